@@ -221,6 +221,129 @@ size_t ssd_mixer_workspace_size(const ssd_mixer_config_t *cfg);
 ssd_status_t mamba2_mixer_forward(const ssd_mixer_config_t *cfg, const ssd_mixer_args_t *args,
                                   void *stream);
 
+/* ---- Gated delta rule ---------------------------------------------------------------------
+ * The recurrent layer whose state update first erases what the state holds along the new key:
+ *
+ *   dt_t    = clamp(softplus(dt_raw_t + dt_bias_h), dt_min, dt_max);  alpha_t = exp(dt_t * A_h)
+ *   beta_t  = beta_scale * sigmoid(b_t)             (beta_sigmoid = 0: beta_scale * b_t)
+ *   k^, q^  = k / sqrt(|k|^2 + qk_eps), q_scale * q / sqrt(|q|^2 + qk_eps)   (qk_norm = 0: k and
+ *             q_scale * q as they are)
+ *   S_t     = alpha_t S_{t-1} + beta_t (v_t - alpha_t S_{t-1} k^_t) k^_t^T   (P x N, fp32)
+ *   y_t     = S_t q^_t                                              (after the update)
+ *
+ * per batch row and head h; the heads of a group share q and k (g = h / (H/G)).  q, k and v are
+ * the rows after any convolution and activation.  The state has the layout of the scan's,
+ * [B, H, P, N] fp32, so the state cache below serves both.  alpha_t in (0, 1] (A <= 0) and
+ * beta_t |k^_t|^2 <= 2 keep the state bounded; other values are computed as they stand. */
+typedef struct {
+  int batch;        /* B >= 1 */
+  int seqlen;       /* L >= 0 tokens in this call (0: h0, or zeros, goes to h_final); ignored by
+                       the decode step */
+  int nheads;       /* H >= 1 value heads, multiple of ngroups */
+  int headdim;      /* P, 64 or 128: rows of the state */
+  int dstate;       /* N; the library supports 128: length of q and k */
+  int ngroups;      /* G >= 1 query/key heads */
+  int qk_norm;      /* 1: q and k are divided by their norms */
+  float qk_eps;     /* > 0 when qk_norm = 1 */
+  float q_scale;    /* 1/sqrt(N) in common use */
+  float dt_min, dt_max; /* clamp of the effective dt (0 and +inf: none) */
+  int dt_softplus;  /* 1: dt = softplus(dt_raw + dt_bias); 0: dt = dt_raw + dt_bias */
+  int beta_sigmoid; /* 1: beta = beta_scale * sigmoid(b); 0: beta = beta_scale * b */
+  float beta_scale; /* 1, or 2 to allow negative eigenvalues of the transition */
+  ssd_dtype_t io_dtype; /* dtype of q, k, v, dt, b and y */
+  ssd_kernel_t kernel;  /* TENSOR: the chunked kernel (bf16 only; UNSUPPORTED otherwise); SIMT: the
+                           token recurrence in fp32; AUTO: whichever is faster for the lengths */
+} ssd_delta_config_t;
+
+typedef struct {
+  const void *q;  long long q_row_stride;   /* [B, L, G*N] */
+  const void *k;  long long k_row_stride;   /* [B, L, G*N] */
+  const void *v;  long long v_row_stride;   /* [B, L, H*P] */
+  const void *dt; long long dt_row_stride;  /* [B, L, H] raw dt */
+  const void *b;  long long b_row_stride;   /* [B, L, H] raw beta */
+  const float *A, *dt_bias;                 /* [H] */
+  const float *h0;      /* [B, H, P, N] initial state or NULL (= 0) */
+  void *y;  long long y_row_stride;         /* [B, L, H*P] output; must not overlap an input */
+  float *h_final;       /* [B, H, P, N] state after the last token, or NULL; may be h0 itself, but
+                           must not overlap it in part */
+  void *workspace;      /* at least ssd_delta_workspace_size() bytes, 256-B aligned (NULL if 0) */
+  size_t workspace_bytes;
+} ssd_delta_args_t;
+
+typedef struct {
+  const void *q;  long long q_row_stride;   /* [B, G*N] */
+  const void *k;  long long k_row_stride;   /* [B, G*N] */
+  const void *v;  long long v_row_stride;   /* [B, H*P] */
+  const void *dt; long long dt_row_stride;  /* [B, H] */
+  const void *b;  long long b_row_stride;   /* [B, H] */
+  const float *A, *dt_bias;                 /* [H] */
+  float *state;         /* [n_slots, H, P, N] states, updated in place */
+  const int *slots;     /* DEVICE [B]: row b's state is state[slots[b]]; NULL: state[b].  A row whose
+                           slot is negative is skipped: its y row and every state stay as they were.
+                           A slot >= n_slots, or one that an earlier row of the batch has, is
+                           skipped too and latches SSD_ERR_DEVICE_BOUNDS. */
+  int n_slots;          /* states in the pool (>= B when slots is NULL) */
+  void *y;  long long y_row_stride;         /* [B, H*P] output */
+} ssd_delta_decode_args_t;
+
+/* Bytes of scratch ssd_delta_prefill needs (0 if the config is invalid, or nothing is needed). */
+size_t ssd_delta_workspace_size(const ssd_delta_config_t *cfg);
+
+/* y and the final state of seqlen tokens per batch row.  Consecutive calls, each fed the previous
+ * call's h_final, give the result of one call (up to rounding).  Accuracy: the state within about
+ * 1e-6 of its size of the fp32 recurrence's, on both paths; y rounded once into io_dtype, from
+ * products that keep 11 bits within a chunk on the chunked path. */
+ssd_status_t ssd_delta_prefill(const ssd_delta_config_t *cfg, const ssd_delta_args_t *args, void *stream);
+
+/* Packed sequences, as in ssd_prefill_varlen: cu_seqlens is a HOST array of nseq + 1 offsets (read
+ * before the call returns, a stream capture included), cfg->batch = 1, cfg->seqlen = all tokens,
+ * h0 / h_final [nseq, H, P, N].  One launch of each kernel for the whole batch.  An empty sequence's
+ * h0 (or zeros) goes to its h_final.  ssd_delta_varlen_workspace_size is 0 for invalid arguments. */
+size_t ssd_delta_varlen_workspace_size(const ssd_delta_config_t *cfg, const int *cu_seqlens, int nseq);
+ssd_status_t ssd_delta_prefill_varlen(const ssd_delta_config_t *cfg, const ssd_delta_args_t *args,
+                                      const int *cu_seqlens, int nseq, void *stream);
+
+/* One token per batch row; the state in place, in fp32 throughout. */
+ssd_status_t ssd_delta_decode_step(const ssd_delta_config_t *cfg, const ssd_delta_decode_args_t *args,
+                                   void *stream);
+
+/* ---- State cache in 8 bits ------------------------------------------------------------------
+ * States that wait (a cached prefix, a preempted sequence) at 33/128 of their fp32 size.  A state
+ * of the scan or of the delta rule, state_elems = H*P*N floats, is cut into blocks of 32
+ * consecutive elements; a block has the scale 2^e, the smallest power of two with max|x| <= 448 * 2^e
+ * (SSD_STATE_E4M3) or 127 * 2^e (SSD_STATE_INT8), and not below 2^-127, and its elements are
+ * x * 2^-e rounded to nearest, ties to even.  Scaling by a power of two is exact, so an element
+ * is off by its one rounding: at most 2^-4 of itself, plus 2^-10 * 2^e near zero (e4m3), or 2^(e-1),
+ * at most 1/127 of the block's largest (int8).  The scale byte is e + 127; 255 marks a block that
+ * held an infinity or a NaN and reads back as NaNs.
+ *
+ *   cache   [n_cache, state_elems]       elements (e4m3 or two's complement int8), 16-byte aligned
+ *   scales  [n_cache, state_elems / 32]  scale bytes, 4-byte aligned
+ *   states  [n_states, state_elems]      fp32, 16-byte aligned
+ *   state_slots, cache_slots  DEVICE [count], NULL: 0 .. count-1
+ *
+ * Entry i of ssd_state_store writes states[state_slots[i]] to cache slot cache_slots[i];
+ * entry i of ssd_state_load writes cache slot cache_slots[i] to states[state_slots[i]].  An entry
+ * with a negative slot on either side is skipped.  A slot outside its array, or a destination that
+ * an earlier entry has, is skipped too and latches SSD_ERR_DEVICE_BOUNDS.  state_elems is a
+ * multiple of 128.  The destination must not overlap the source. */
+typedef enum { SSD_STATE_E4M3 = 0, SSD_STATE_INT8 = 1 } ssd_state_format_t;
+
+typedef struct {
+  ssd_state_format_t format;
+  long long state_elems;
+  int count;                  /* entries, >= 0 */
+  const int *state_slots;
+  const int *cache_slots;
+  int n_states, n_cache;      /* with NULL slots, >= count */
+  float *states;              /* read by store, written by load */
+  void *cache;                /* written by store, read by load */
+  unsigned char *scales;
+} ssd_state_cache_args_t;
+
+ssd_status_t ssd_state_store(const ssd_state_cache_args_t *args, void *stream);
+ssd_status_t ssd_state_load(const ssd_state_cache_args_t *args, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *ssd_status_string(ssd_status_t status);
 

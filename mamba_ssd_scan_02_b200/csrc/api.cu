@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "delta_plan.h"
 #include "plan.h"
 
 namespace ssd {
@@ -28,8 +29,7 @@ std::atomic<unsigned long long> g_stall_wait_ns{0};
 std::atomic<int> g_bounds_denom{1};
 
 constexpr int kMaxDevices = 64;
-constexpr long long kTargetCtas = 2 * 148;  // scan CTAs wanted in flight (2 per B200 SM)
-constexpr size_t kAlign = 256;
+}  // namespace
 
 int *device_error_ptr() {
   static std::mutex mu;
@@ -44,6 +44,12 @@ int *device_error_ptr() {
   }
   return ptrs[dev];
 }
+
+int bounds_denom() { return g_bounds_denom.load(); }
+
+namespace {
+constexpr long long kTargetCtas = 2 * 148;  // scan CTAs wanted in flight (2 per B200 SM)
+constexpr size_t kAlign = 256;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }

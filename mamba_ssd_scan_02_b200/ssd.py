@@ -73,6 +73,35 @@ class MixerArgs(ctypes.Structure):
                 ("workspace", vp), ("workspace_bytes", c_size)]
 
 
+class DeltaConfig(ctypes.Structure):
+    _fields_ = [("batch", c_int), ("seqlen", c_int), ("nheads", c_int), ("headdim", c_int),
+                ("dstate", c_int), ("ngroups", c_int), ("qk_norm", c_int), ("qk_eps", c_float),
+                ("q_scale", c_float), ("dt_min", c_float), ("dt_max", c_float),
+                ("dt_softplus", c_int), ("beta_sigmoid", c_int), ("beta_scale", c_float),
+                ("io_dtype", c_int), ("kernel", c_int)]
+
+
+class DeltaArgs(ctypes.Structure):
+    _fields_ = [("q", vp), ("q_row_stride", c_ll), ("k", vp), ("k_row_stride", c_ll), ("v", vp),
+                ("v_row_stride", c_ll), ("dt", vp), ("dt_row_stride", c_ll), ("b", vp),
+                ("b_row_stride", c_ll), ("A", vp), ("dt_bias", vp), ("h0", vp), ("y", vp),
+                ("y_row_stride", c_ll), ("h_final", vp), ("workspace", vp),
+                ("workspace_bytes", c_size)]
+
+
+class DeltaDecodeArgs(ctypes.Structure):
+    _fields_ = [("q", vp), ("q_row_stride", c_ll), ("k", vp), ("k_row_stride", c_ll), ("v", vp),
+                ("v_row_stride", c_ll), ("dt", vp), ("dt_row_stride", c_ll), ("b", vp),
+                ("b_row_stride", c_ll), ("A", vp), ("dt_bias", vp), ("state", vp), ("slots", vp),
+                ("n_slots", c_int), ("y", vp), ("y_row_stride", c_ll)]
+
+
+class StateCacheArgs(ctypes.Structure):
+    _fields_ = [("format", c_int), ("state_elems", c_ll), ("count", c_int), ("state_slots", vp),
+                ("cache_slots", vp), ("n_states", c_int), ("n_cache", c_int), ("states", vp),
+                ("cache", vp), ("scales", vp)]
+
+
 class TraceRecord(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("ms", c_float)]
 
@@ -81,7 +110,9 @@ EXPORTS = ("ssd_workspace_size", "ssd_prefill", "ssd_decode_step", "ssd_mixer_wo
            "mamba2_mixer_forward", "ssd_status_string", "ssd_get_device_error", "ssd_version",
            "ssd_trace_enable", "ssd_trace_read", "ssd_prefill_noalloc", "ssd_varlen_workspace_size",
            "ssd_prefill_varlen", "ssd_test_stall_scan", "ssd_prefill_span_state", "ssd_span_prefix",
-           "ssd_debug_bounds_build", "ssd_test_bounds_scale")
+           "ssd_debug_bounds_build", "ssd_test_bounds_scale", "ssd_delta_workspace_size",
+           "ssd_delta_prefill", "ssd_delta_varlen_workspace_size", "ssd_delta_prefill_varlen",
+           "ssd_delta_decode_step", "ssd_state_store", "ssd_state_load")
 
 def debug_bounds_build() -> bool:
     """True for the library built with device-side index checks (libssd_debug.so)."""
@@ -149,6 +180,21 @@ def load(path: str = LIB_PATH):
     lib.ssd_trace_enable.argtypes = [c_int]
     lib.ssd_trace_read.restype = c_int
     lib.ssd_trace_read.argtypes = [ctypes.POINTER(TraceRecord), c_int]
+    lib.ssd_delta_workspace_size.restype = c_size
+    lib.ssd_delta_workspace_size.argtypes = [ctypes.POINTER(DeltaConfig)]
+    lib.ssd_delta_prefill.restype = c_int
+    lib.ssd_delta_prefill.argtypes = [ctypes.POINTER(DeltaConfig), ctypes.POINTER(DeltaArgs), vp]
+    lib.ssd_delta_varlen_workspace_size.restype = c_size
+    lib.ssd_delta_varlen_workspace_size.argtypes = [ctypes.POINTER(DeltaConfig), ctypes.POINTER(c_int), c_int]
+    lib.ssd_delta_prefill_varlen.restype = c_int
+    lib.ssd_delta_prefill_varlen.argtypes = [ctypes.POINTER(DeltaConfig), ctypes.POINTER(DeltaArgs),
+                                             ctypes.POINTER(c_int), c_int, vp]
+    lib.ssd_delta_decode_step.restype = c_int
+    lib.ssd_delta_decode_step.argtypes = [ctypes.POINTER(DeltaConfig), ctypes.POINTER(DeltaDecodeArgs), vp]
+    lib.ssd_state_store.restype = c_int
+    lib.ssd_state_store.argtypes = [ctypes.POINTER(StateCacheArgs), vp]
+    lib.ssd_state_load.restype = c_int
+    lib.ssd_state_load.argtypes = [ctypes.POINTER(StateCacheArgs), vp]
     _lib = lib
     return lib
 
@@ -424,6 +470,239 @@ def mixer_forward(cfg: dict, hidden, rms_w, W_in, W_out, A, D, dt_bias, conv_w, 
     _check(lib.mamba2_mixer_forward(ctypes.byref(m), ctypes.byref(a), _stream(stream)),
            "mamba2_mixer_forward")
     return out
+
+
+# ---- gated delta rule -------------------------------------------------------------------------
+def make_delta_config(cfg: dict, batch: int, seqlen: int, kernel: int | None = None) -> DeltaConfig:
+    """C config of the delta rule: nheads and ngroups of cfg, and, where it has them, headdim (64),
+    dstate (128), dtype ("bf16" or "f32"), qk_norm (True), qk_eps (1e-6), q_scale
+    (1/sqrt(dstate)), dt_min (0), dt_max (inf), dt_softplus (True), beta_sigmoid (True),
+    beta_scale (1) and kernel."""
+    get = cfg.get
+    N = get("dstate", 128)
+    return DeltaConfig(
+        batch, seqlen, cfg["nheads"], get("headdim", 64), N, cfg["ngroups"],
+        int(get("qk_norm", True)), get("qk_eps", 1e-6), get("q_scale", 1.0 / math.sqrt(N)),
+        get("dt_min", 0.0), get("dt_max", math.inf), int(get("dt_softplus", True)),
+        int(get("beta_sigmoid", True)), get("beta_scale", 1.0),
+        SSD_BF16 if get("dtype", "bf16") == "bf16" else SSD_F32,
+        get("kernel", KERNEL_AUTO) if kernel is None else kernel)
+
+
+def _check_arg(t, name, dtype, device, shape):
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} {shape} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _check_dense(t, name, dtype, device, shape):
+    _check_arg(t, name, dtype, device, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, name, dtype, device, shape):
+    """(pointer, elements between consecutive rows) of a token tensor [..., width] whose rows are
+    evenly spaced: [B, L, width] rows are L * stride apart between batch rows."""
+    _check_arg(t, name, dtype, device, shape)
+    st = t.stride()
+    many = [i for i in range(len(shape) - 1) if shape[i] != 1]
+    if st[-1] != 1 and shape[-1] > 1 and 0 not in shape:
+        raise ValueError(f"{name}: channels must be contiguous")
+    if not many or 0 in shape:
+        # at most one row: any stride that holds it and keeps the alignment rule
+        return t.data_ptr(), (shape[-1] + 7) // 8 * 8
+    if len(many) == 2 and st[0] != shape[1] * st[1]:
+        raise ValueError(f"{name}: batch rows must be seqlen * row_stride apart")
+    return t.data_ptr(), st[many[-1]]
+
+
+def _call(fn, where, device, stream, made, *args):
+    """Runs fn(*args, stream) with `device` current.  `stream` None: the device's current stream.
+    Tensors in `made` were allocated here, under the current stream: on another one, the
+    allocator is told so."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"{where}: tensors must be on a CUDA device, got {device}")
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    else:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device != device:
+            raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {device}")
+        handle = stream.cuda_stream
+        for t in made:
+            t.record_stream(stream)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status != 0:
+        raise SsdError(status, where)
+
+
+def delta_workspace_size(cfg: dict, batch: int, seqlen: int, kernel: int | None = None) -> int:
+    """ssd_delta_workspace_size for batch rows of seqlen tokens."""
+    return load().ssd_delta_workspace_size(ctypes.byref(make_delta_config(cfg, batch, seqlen, kernel)))
+
+
+def delta_varlen_workspace_size(cfg: dict, cu_seqlens, kernel: int | None = None) -> int:
+    """ssd_delta_varlen_workspace_size for the packed batch with offsets cu_seqlens."""
+    cu = [int(v) for v in cu_seqlens]
+    c = make_delta_config(cfg, 1, cu[-1], kernel)
+    return load().ssd_delta_varlen_workspace_size(ctypes.byref(c), (c_int * len(cu))(*cu), len(cu) - 1)
+
+
+def _delta_prefill(cfg, c, cu, nseq, lead, q, k, v, dt, b, A, dt_bias, h0, y, h_final, workspace,
+                   stream, want_state):
+    import torch
+    lib = load()
+    H, P, N, G = c.nheads, c.headdim, c.dstate, c.ngroups
+    dev, dtype, f32 = q.device, io_dtype(cfg), torch.float32
+    made = []
+
+    def new(*shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        made.append(t)
+        return t
+
+    if y is None:
+        y = new(*lead, H * P, dtype=dtype)
+    if h_final is None and want_state:
+        h_final = new(nseq, H, P, N, dtype=f32)
+    if workspace is None:
+        n = (lib.ssd_delta_varlen_workspace_size(ctypes.byref(c), cu, nseq) if cu is not None
+             else lib.ssd_delta_workspace_size(ctypes.byref(c)))
+        workspace = new(n, dtype=torch.uint8) if n else None
+    args = DeltaArgs(
+        *_rows(q, "q", dtype, dev, (*lead, G * N)), *_rows(k, "k", dtype, dev, (*lead, G * N)),
+        *_rows(v, "v", dtype, dev, (*lead, H * P)), *_rows(dt, "dt", dtype, dev, (*lead, H)),
+        *_rows(b, "b", dtype, dev, (*lead, H)), _check_dense(A, "A", f32, dev, (H,)),
+        _check_dense(dt_bias, "dt_bias", f32, dev, (H,)),
+        None if h0 is None else _check_dense(h0, "h0", f32, dev, (nseq, H, P, N)),
+        *_rows(y, "y", dtype, dev, (*lead, H * P)),
+        None if h_final is None else _check_dense(h_final, "h_final", f32, dev, (nseq, H, P, N)),
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size())
+    if cu is None:
+        _call(lib.ssd_delta_prefill, "ssd_delta_prefill", dev, stream, made, ctypes.byref(c), ctypes.byref(args))
+    else:
+        _call(lib.ssd_delta_prefill_varlen, "ssd_delta_prefill_varlen", dev, stream, made,
+              ctypes.byref(c), ctypes.byref(args), cu, nseq)
+    return y, h_final
+
+
+def delta_prefill(cfg: dict, q, k, v, dt, b, A, dt_bias, h0=None, *, y=None, h_final=None,
+                  workspace=None, stream=None, want_state: bool = True, kernel: int | None = None):
+    """ssd_delta_prefill: the gated delta rule over q, k [B, L, G*N], v [B, L, H*P] and the raw gates
+    dt, b [B, L, H] (see make_delta_config for cfg), from the state h0 [B, H, P, N]; returns
+    (y [B, L, H*P], h_final [B, H, P, N], or None when want_state is False)."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [batch, seqlen, ngroups * dstate], got {tuple(q.shape)}")
+    Bn, L = q.shape[0], q.shape[1]
+    c = make_delta_config(cfg, Bn, L, kernel)
+    return _delta_prefill(cfg, c, None, Bn, (Bn, L), q, k, v, dt, b, A, dt_bias, h0, y, h_final,
+                          workspace, stream, want_state)
+
+
+def delta_prefill_varlen(cfg: dict, cu_seqlens, q, k, v, dt, b, A, dt_bias, h0=None, *, y=None,
+                         h_final=None, workspace=None, stream=None, want_state: bool = True,
+                         kernel: int | None = None):
+    """ssd_delta_prefill_varlen: packed sequences (q, k [T, G*N], ... with T = cu_seqlens[-1], host
+    offsets cu_seqlens), each from its own state h0[i]; returns (y [T, H*P], h_final
+    [nseq, H, P, N], or None when want_state is False)."""
+    cu = [int(v_) for v_ in cu_seqlens]
+    if len(cu) < 2:
+        raise ValueError("cu_seqlens needs at least two offsets")
+    c = make_delta_config(cfg, 1, cu[-1], kernel)
+    return _delta_prefill(cfg, c, (c_int * len(cu))(*cu), len(cu) - 1, (cu[-1],), q, k, v, dt, b, A,
+                          dt_bias, h0, y, h_final, workspace, stream, want_state)
+
+
+def delta_decode_step(cfg: dict, q_t, k_t, v_t, dt_t, b_t, A, dt_bias, state, slots=None, *, y=None,
+                      stream=None):
+    """ssd_delta_decode_step: one token per row, q_t, k_t [B, G*N], v_t [B, H*P], dt_t, b_t [B, H].
+    state [n_slots, H, P, N] is updated in place: row i's state is state[slots[i]] (int32, on the
+    device), or state[i] without slots; a row with a negative slot is skipped, its y row left as
+    it was (zero, where y is not given).  Returns y [B, H*P]."""
+    import torch
+    lib = load()
+    if q_t.dim() != 2 or state.dim() != 4:
+        raise ValueError("q_t must be [batch, ngroups * dstate] and state [n_slots, nheads, headdim, dstate]")
+    Bn = q_t.shape[0]
+    c = make_delta_config(cfg, Bn, 1)
+    H, P, N, G = c.nheads, c.headdim, c.dstate, c.ngroups
+    dev, dtype, f32 = q_t.device, io_dtype(cfg), torch.float32
+    made = []
+    if y is None:
+        y = (torch.empty if slots is None else torch.zeros)((Bn, H * P), dtype=dtype, device=dev)
+        made.append(y)
+    a = DeltaDecodeArgs(
+        *_rows(q_t, "q_t", dtype, dev, (Bn, G * N)), *_rows(k_t, "k_t", dtype, dev, (Bn, G * N)),
+        *_rows(v_t, "v_t", dtype, dev, (Bn, H * P)), *_rows(dt_t, "dt_t", dtype, dev, (Bn, H)),
+        *_rows(b_t, "b_t", dtype, dev, (Bn, H)), _check_dense(A, "A", f32, dev, (H,)),
+        _check_dense(dt_bias, "dt_bias", f32, dev, (H,)),
+        _check_dense(state, "state", f32, dev, (state.shape[0], H, P, N)),
+        None if slots is None else _check_dense(slots, "slots", torch.int32, dev, (Bn,)),
+        state.shape[0], *_rows(y, "y", dtype, dev, (Bn, H * P)))
+    _call(lib.ssd_delta_decode_step, "ssd_delta_decode_step", dev, stream, made, ctypes.byref(c), ctypes.byref(a))
+    return y
+
+
+# ---- state cache in 8 bits --------------------------------------------------------------------
+STATE_E4M3, STATE_INT8 = 0, 1
+
+
+def state_cache(n_slots: int, state_shape, fmt: str = "e4m3", device="cuda"):
+    """(cache, scales) of n_slots places for states of state_shape (such as (H, P, N)): the elements
+    [n_slots, *state_shape] in float8_e4m3fn or int8, and the scale bytes [n_slots, ..., N / 32].
+    All zeros: every place reads back as zeros."""
+    import torch
+    *lead, n = state_shape
+    if n % 32 != 0:
+        raise ValueError("the last dimension of a state must be a multiple of 32")
+    kind = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}[fmt]
+    cache = torch.zeros((n_slots, *lead, n), dtype=torch.uint8, device=device).view(kind)
+    return cache, torch.zeros((n_slots, *lead, n // 32), dtype=torch.uint8, device=device)
+
+
+def _state_cache_call(name, states, cache, scales, state_slots, cache_slots, stream):
+    import torch
+    dev = states.device
+    fmt = {torch.float8_e4m3fn: STATE_E4M3, torch.int8: STATE_INT8}.get(cache.dtype)
+    if fmt is None:
+        raise ValueError(f"cache must be float8_e4m3fn or int8, got {cache.dtype}")
+    if states.dim() < 2 or states.shape[-1] % 32 != 0:
+        raise ValueError(f"states must be [n, ..., a multiple of 32], got {tuple(states.shape)}")
+    shape = tuple(states.shape[1:])
+    ps = _check_dense(states, "states", torch.float32, dev, (states.shape[0], *shape))
+    pc = _check_dense(cache, "cache", cache.dtype, dev, (cache.shape[0], *shape))
+    pf = _check_dense(scales, "scales", torch.uint8, dev, (cache.shape[0], *shape[:-1], shape[-1] // 32))
+    count = len(state_slots if state_slots is not None else cache_slots if cache_slots is not None else states)
+    a = StateCacheArgs(
+        fmt, math.prod(shape), count,
+        None if state_slots is None else _check_dense(state_slots, "state_slots", torch.int32, dev, (count,)),
+        None if cache_slots is None else _check_dense(cache_slots, "cache_slots", torch.int32, dev, (count,)),
+        states.shape[0], cache.shape[0], ps, pc, pf)
+    _call(getattr(load(), name), name, dev, stream, (), ctypes.byref(a))
+
+
+def state_store(states, cache, scales, state_slots=None, cache_slots=None, *, stream=None):
+    """ssd_state_store: puts states[state_slots[i]] (fp32) into place cache_slots[i] of a cache made
+    by state_cache.  Slots are int32 on the device; without state_slots the states are taken in
+    order, without cache_slots the places.  Returns (cache, scales)."""
+    _state_cache_call("ssd_state_store", states, cache, scales, state_slots, cache_slots, stream)
+    return cache, scales
+
+
+def state_load(cache, scales, states, state_slots=None, cache_slots=None, *, stream=None):
+    """ssd_state_load: reads place cache_slots[i] of the cache back into states[state_slots[i]];
+    returns states."""
+    _state_cache_call("ssd_state_load", states, cache, scales, state_slots, cache_slots, stream)
+    return states
 
 
 def get_device_error(stream=None) -> int:
