@@ -80,7 +80,14 @@ bool packed(const ssd_delta_config_t *c, const int *cu, int nseq, Batch *b) {
   return true;
 }
 
-bool uses_chunks(const ssd_delta_config_t *, const Batch &) { return false; }
+// The longest sequence from which AUTO takes the chunked kernel.
+constexpr int kChunkedFrom = 96;
+
+bool uses_chunks(const ssd_delta_config_t *c, const Batch &b) {
+  if (b.rows == 0 || c->kernel == SSD_KERNEL_SIMT) return false;
+  if (c->kernel == SSD_KERNEL_TENSOR) return true;
+  return c->io_dtype == SSD_BF16 && b.longest >= kChunkedFrom && tc_scan_available();
+}
 
 struct Layout {
   size_t tiles, gates, ints, total;
@@ -188,6 +195,13 @@ ssd_status_t run_prefill(const ssd_delta_config_t *c, const ssd_delta_args_t *a,
     const cudaError_t e = traced("ssd_put_ints", s, [&] { return launch_put_ints(dev, ints.data(), (int)ints.size(), s); });
     if (e != cudaSuccess) return SSD_ERR_CUDA;
     p.cu = dev; p.chunk0 = dev + b.nseq + 1; p.order = p.chunk0 + b.nseq + 1;
+  }
+  if (uses_chunks(c, b)) {
+    p.tiles = reinterpret_cast<unsigned char *>(ws + l.tiles);
+    p.gates = reinterpret_cast<float *>(ws + l.gates);
+    const cudaError_t e = traced("ssd_delta_front", s, [&] { return launch_delta_front(p, s); });
+    if (e != cudaSuccess) return SSD_ERR_CUDA;
+    return from_cuda(traced("ssd_delta_chunks", s, [&] { return launch_delta_chunks(p, s); }));
   }
   return from_cuda(traced("ssd_delta_recurrent", s, [&] { return launch_delta_recurrent(p, s); }));
 }

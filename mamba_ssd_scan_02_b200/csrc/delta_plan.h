@@ -53,6 +53,10 @@ struct DeltaPlan {
 cudaError_t launch_delta_recurrent(const DeltaPlan &p, cudaStream_t s);
 cudaError_t launch_delta_decode(const DeltaPlan &p, cudaStream_t s);
 
+// chunked on the tensor cores (delta_tc.cu): the front end writes tiles and gates, the chunks follow
+cudaError_t launch_delta_front(const DeltaPlan &p, cudaStream_t s);
+cudaError_t launch_delta_chunks(const DeltaPlan &p, cudaStream_t s);
+
 struct StateCachePlan {
   ssd_state_format_t format;
   long long elems;
