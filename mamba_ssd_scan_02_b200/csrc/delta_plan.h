@@ -13,9 +13,10 @@ constexpr int kDeltaChunk = 64;
 //  tile   per (chunk, group): the fp16 operand image of 64 key rows then 64 query rows, two halves
 //         of 64 columns, each 128 rows x 128 bytes with the 128-byte swizzle, then the row
 //         factors rho_k[64], rho_q[64] (fp32)
-//  gates  per (chunk, head): prefix sums of log2(alpha) as two floats hi[64], lo[64], and beta[64]
+//  gates  per (chunk, head), 64 floats each: the prefix sums cs of log2(alpha) as two floats hi and lo,
+//         beta, 2^cs, rho_k 2^{cs at the end of the block of 32 - cs}, rho_k 2^{cs at the chunk's end - cs}
 constexpr long long kDeltaTileBytes = 32768 + 512;
-constexpr long long kDeltaGateBytes = 768;
+constexpr long long kDeltaGateBytes = 6 * 256;
 
 struct DeltaPlan {
   int B, L, H, P, G, hpg;  // L: the longest sequence of a packed batch
