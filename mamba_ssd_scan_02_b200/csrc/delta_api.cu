@@ -90,7 +90,7 @@ bool uses_chunks(const ssd_delta_config_t *c, const Batch &b) {
 }
 
 struct Layout {
-  size_t tiles, gates, ints, total;
+  size_t tiles, records, ints, total;
 };
 
 Layout layout(const ssd_delta_config_t *c, const Batch &b) {
@@ -99,8 +99,8 @@ Layout layout(const ssd_delta_config_t *c, const Batch &b) {
   if (uses_chunks(c, b)) {
     l.tiles = off;
     off = round_up(off + (size_t)(b.chunks * c->ngroups * kDeltaTileBytes), kAlign);
-    l.gates = off;
-    off = round_up(off + (size_t)(b.chunks * c->nheads * kDeltaGateBytes), kAlign);
+    l.records = off;
+    off = round_up(off + (size_t)(b.chunks * c->nheads * kDeltaRecordBytes), kAlign);
   }
   l.ints = off;
   if (b.cu) off = round_up(off + (size_t)(3 * (long long)b.nseq + 2) * sizeof(int), kAlign);
@@ -198,7 +198,7 @@ ssd_status_t run_prefill(const ssd_delta_config_t *c, const ssd_delta_args_t *a,
   }
   if (uses_chunks(c, b)) {
     p.tiles = reinterpret_cast<unsigned char *>(ws + l.tiles);
-    p.gates = reinterpret_cast<float *>(ws + l.gates);
+    p.records = reinterpret_cast<unsigned char *>(ws + l.records);
     const cudaError_t e = traced("ssd_delta_front", s, [&] { return launch_delta_front(p, s); });
     if (e != cudaSuccess) return SSD_ERR_CUDA;
     return from_cuda(traced("ssd_delta_chunks", s, [&] { return launch_delta_chunks(p, s); }));

@@ -9,14 +9,14 @@ namespace ssd {
 
 // Tokens per chunk of the tensor-core kernel.
 constexpr int kDeltaChunk = 64;
-// One chunk's workspace records, written by the front end and read by the chunked kernel:
-//  tile   per (chunk, group): the fp16 operand image of 64 key rows then 64 query rows, two halves
-//         of 64 columns, each 128 rows x 128 bytes with the 128-byte swizzle, then the row
-//         factors rho_k[64], rho_q[64] (fp32)
-//  gates  per (chunk, head), 64 floats each: the prefix sums cs of log2(alpha) as two floats hi and lo,
-//         beta, 2^cs, rho_k 2^{cs at the end of the block of 32 - cs}, rho_k 2^{cs at the chunk's end - cs}
+// One chunk's workspace records, written by the front end and read by the chunk kernel:
+//  tile    per (chunk, group): the fp16 operand image of 64 key rows then 64 query rows, two halves
+//          of 64 columns, each 128 rows x 128 bytes with the 128-byte swizzle; then the row factors
+//          rho_k[64], rho_q[64] (fp32)
+//  record  per (chunk, head): the operand images of T~^T hi, T~^T lo and A T (64 rows x 128 bytes each,
+//          swizzled); then beta[64], 2^cs[64] and rho_k 2^{cs at the chunk's end - cs}[64] (fp32)
 constexpr long long kDeltaTileBytes = 32768 + 512;
-constexpr long long kDeltaGateBytes = 6 * 256;
+constexpr long long kDeltaRecordBytes = 3 * 8192 + 3 * 256;
 
 struct DeltaPlan {
   int B, L, H, P, G, hpg;  // L: the longest sequence of a packed batch
@@ -26,6 +26,7 @@ struct DeltaPlan {
   const int *cu, *chunk0, *order;
   long long rows;      // token rows
   long long n_chunks;  // over all sequences
+  int heads_per_cta;   // of the front end
   int qk_norm;
   float qk_eps, q_scale;
   float dt_min, dt_max;
@@ -43,8 +44,7 @@ struct DeltaPlan {
   const int *slots;
   int n_slots;
   // workspace of the chunked kernel
-  unsigned char *tiles;
-  float *gates;
+  unsigned char *tiles, *records;
   int *err;
   // elements of the y and state buffers, for the debug build's index checks
   long long y_extent, state_extent;
@@ -54,7 +54,8 @@ struct DeltaPlan {
 cudaError_t launch_delta_recurrent(const DeltaPlan &p, cudaStream_t s);
 cudaError_t launch_delta_decode(const DeltaPlan &p, cudaStream_t s);
 
-// chunked on the tensor cores (delta_tc.cu): the front end writes tiles and gates, the chunks follow
+// chunked on the tensor cores: the front end (delta_prep.cu) writes tiles and records, the chunks follow
+// (delta_tc.cu)
 cudaError_t launch_delta_front(const DeltaPlan &p, cudaStream_t s);
 cudaError_t launch_delta_chunks(const DeltaPlan &p, cudaStream_t s);
 
