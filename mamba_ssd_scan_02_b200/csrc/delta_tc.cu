@@ -8,10 +8,10 @@
 // K_i exact in fp16.  The decays and the rho are a similarity of L: with
 //   L~_ij = beta_i rho_i^2 K_i.K_j  (j < i),   T~ = (I + L~)^-1,
 // (I + L)^-1_ij = T~_ij 2^{cs_i - cs_j} rho_j / rho_i, so that
-//   S' = 2^{cs_C} S + sum_j (rho_j 2^{cs_C - cs_j} R_j) M_j^T,          M = K^T T~          (N x 64)
+//   S' = 2^{cs_C} S + sum_j R_j (rho_j 2^{cs_C - cs_j} M_j)^T,          M = K^T T~          (N x 64)
 //   y_t = 2^{cs_t} S q_t + sum_j 2^{cs_t - cs_j} rho_j (A~ T~)_tj R_j,   A~_ti = q_t.K_i     (i <= t)
 // The inverse, M and A~ T~ know no decay, and nothing of them depends on the state: the chain from chunk
-// to chunk is two dependent products, K S^T (which gives R) and M R~.  One CTA carries 64 state rows
+// to chunk is two dependent products, K S^T (which gives R) and M R.  One CTA carries 64 state rows
 // of one head through the sequence (the rows are independent given K, so a head of 128 rows is two
 // CTAs).
 //
@@ -27,11 +27,14 @@
 // beside it) is rounded to 11 bits: y is then rounded to bf16's 8.
 //
 // Roles (16 warps, so that a thread may have 128 registers).  Warps 0-7, the chain: S into its operand, R
-// from K S^T, the new S, y.  Warps 8-11 bring M (of the chunk after) into its operand.  Warps 12 and 13
-// issue the MMAs of the chain and of M (an issuing thread is held up for about as long as its MMAs
-// run), warp 14 loads (bulk copies of the front end's tiles and records and of the rows of V), warp 15
-// finds the largest |V| of each chunk.  Hand-overs are mbarriers; every wait is bounded: a timeout makes
-// every role leave and latches SSD_ERR_TIMEOUT.
+// from K S^T, the new S, y.  Their two halves, 32 state rows each, are chains of their own, so that the
+// conversions of the one run beside the products of the other.  Warps 8-11 bring M (of the chunk
+// after) into its operand.  Warps 12 and 13 issue the MMAs of the two chains, warp 15 those of M, warp
+// 14 loads (TMA tiles of V, bulk copies of the front end's tiles and records) and finds the largest |V|
+// of each chunk.  Hand-overs are mbarriers; every wait is bounded: a timeout makes every role leave and
+// latches SSD_ERR_TIMEOUT.
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
 #include "delta_mma.cuh"
 #include "delta_plan.h"
@@ -46,82 +49,93 @@ using namespace delta;
 
 constexpr int C = kDeltaChunk;
 constexpr int kThreads = 16 * 32;
-constexpr int kStages = 2;
 constexpr uint32_t kHalf = 16384;  // 128 rows x 128 bytes
-// stage
+// Two rings of stages: the group's tile (from L2, as a rule: 16 heads or so share it), two deep, and the
+// head's record and V, three deep, since a load takes about as long as a chunk.
 constexpr uint32_t OFF_RHOK = 2 * kHalf;          // the tile's row factors follow its operands
 constexpr uint32_t OFF_RHOQ = OFF_RHOK + 256;
-constexpr uint32_t OFF_T = 33 * 1024;             // the record: T~^T hi, lo, A T; three arrays of 64 floats
-constexpr uint32_t OFF_AT = OFF_T + 2 * 8192;
-constexpr uint32_t OFF_BETA = OFF_T + 3 * 8192;
+constexpr uint32_t kTile = 33 * 1024;
+constexpr int kRecStages = 3;
+constexpr uint32_t OFF_T = 0;                     // the record: T~^T hi, lo, A T; three arrays of 64 floats
+constexpr uint32_t OFF_AT = 2 * 8192;
+constexpr uint32_t OFF_BETA = 3 * 8192;
 constexpr uint32_t OFF_GAMMA = OFF_BETA + 256;
 constexpr uint32_t OFF_END = OFF_GAMMA + 256;
-constexpr uint32_t OFF_V = OFF_END + 256;         // 64 rows of 128 bytes, 144 apart (no bank conflicts)
-constexpr uint32_t kVPitch = 144;
-constexpr uint32_t kStage = (OFF_V + C * kVPitch + 1023) / 1024 * 1024;
-static_assert(OFF_RHOQ + 256 == kDeltaTileBytes && kDeltaTileBytes <= OFF_T && OFF_V - OFF_T == kDeltaRecordBytes, "as loaded");
+constexpr uint32_t OFF_V = (OFF_END + 256 + 1023) / 1024 * 1024;  // 64 rows of 128 bytes, swizzled
+constexpr uint32_t kRec = OFF_V + 8192;
+static_assert(OFF_RHOQ + 256 == kDeltaTileBytes && kDeltaTileBytes <= kTile && OFF_END + 256 == kDeltaRecordBytes, "as loaded");
 // CTA
-constexpr uint32_t OFF_SB = kStages * kStage;     // S operand: [n][p] hi, then lo (128 rows x 128 bytes each)
-constexpr uint32_t OFF_RB = OFF_SB + 2 * kHalf;   // R operands: [token][p] R~ hi, lo; R (64 rows x 128 bytes each)
-constexpr uint32_t OFF_MAXS = OFF_RB + 3 * 8192;  // largest |S| per chain warp, two chunks
-constexpr uint32_t OFF_MAXV = OFF_MAXS + 64;      // bound of what the chunk adds, per stage
+constexpr uint32_t OFF_REC = 2 * kTile;
+constexpr uint32_t OFF_SB = OFF_REC + kRecStages * kRec;  // S operands of the halves: [n][32 p hi, 32 p lo], 128 rows each
+constexpr uint32_t OFF_R = OFF_SB + 2 * kHalf;    // R operands of the halves: [token][32 p hi, 32 p lo], 64 rows each
+constexpr uint32_t OFF_MAXS = OFF_R + 2 * 8192;      // largest |S| per chain warp, two chunks
+constexpr uint32_t OFF_MAXV = OFF_MAXS + 64;      // bound of what the chunk adds, per record stage
 constexpr uint32_t OFF_BAR = OFF_MAXV + 64;
 // A barrier that can complete again before every waiter has seen the phase before has one copy per
 // buffer, so that a parity test never sees two phases at once.
 enum {
-  BAR_FULL,                        // [2] stage loaded
-  BAR_EMPTY = BAR_FULL + kStages,  // [2] its last product is done (and every read before it)
-  BAR_MAXV = BAR_EMPTY + kStages,  // [2] bound of what the chunk adds known
-  BAR_M = BAR_MAXV + kStages,      // [2] M done
+  BAR_TFULL,                       // [2] tile loaded
+  BAR_TEMPTY = BAR_TFULL + 2,      // [2] its last products, and those of its M, are done (2 issuers)
+  BAR_RFULL = BAR_TEMPTY + 2,      // [3] record and V loaded
+  BAR_REMPTY = BAR_RFULL + kRecStages,   // [3] released as the tile (2 issuers)
+  BAR_READY = BAR_REMPTY + kRecStages,   // [3] record, V and tile loaded, and the bound of what the chunk adds known
+  BAR_M = BAR_READY + kRecStages,   // [2] M done
   BAR_MREADY = BAR_M + 2,          // [2] M operand in tensor memory (4 warps)
-  BAR_SREADY = BAR_MREADY + 2,     // S operand written (8 warps)
-  BAR_D1,                          // K S^T, Q S^T done
-  BAR_RREADY,                      // R operands written, D1 read (8 warps)
-  BAR_S,                           // M R~ done
-  BAR_O,                           // A T R done
-  BAR_DONE,                        // [2] nothing of an issuer's left in flight
-  kNumBars = BAR_DONE + 2
+  BAR_SREADY = BAR_MREADY + 2,     // [2 halves] S operand written (4 warps)
+  BAR_D1 = BAR_SREADY + 2,         // [2 halves] K S^T, Q S^T done
+  BAR_RREADY = BAR_D1 + 2,         // [2 halves] R operand written, D1 read (4 warps)
+  BAR_S = BAR_RREADY + 2,          // [2 halves] M R done
+  BAR_O = BAR_S + 2,               // [2 halves] A T R done
+  BAR_DONE = BAR_O + 2,            // [3] nothing of an issuer's left in flight
+  kNumBars = BAR_DONE + 3
 };
 constexpr uint32_t OFF_MISC = OFF_BAR + 8 * 32;   // [0] TMEM base, [1] abort flag
 constexpr uint32_t kSmem = OFF_MISC + 16 + 1024;  // room to align the base to 1024 bytes
 static_assert(kNumBars <= 32 && kSmem <= 232448, "shared memory");
-static_assert(OFF_SB % 1024 == 0 && OFF_RB % 1024 == 0 && OFF_T % 1024 == 0, "swizzle alignment");
+static_assert(OFF_SB % 1024 == 0 && OFF_R % 1024 == 0 && OFF_T % 1024 == 0, "swizzle alignment");
 
 // TMEM columns.  K rows are lanes 0-63 of D1, Q rows lanes 64-127, as are the rows of A T R (lanes 0-63
-// of it are never used).  The M operand replaces M: tokens 32 b .. 32 b + 31 lie in the columns 32 b .. of
-// their own 32 fp32 columns, hi first, lo 16 columns on.
-constexpr uint32_t TM_M = 0, TM_D1 = 128, TM_S = 256, TM_O = 320, TM_COLS = 512;
+// of it are never used).  D1 and S have per half 32 columns of the products with hi, 32 of those with
+// lo, O 32 columns.  The M operand replaces M: tokens 32 b .. 32 b + 31 lie in the columns 32 b .. of their own 32 fp32
+// columns, hi first, lo 16 columns on.
+constexpr uint32_t TM_M = 0, TM_D1 = 128, TM_S = 256, TM_O = 384, TM_COLS = 512;
 
-constexpr uint32_t IDESC_D1 = idesc_f16(128, 128, false, true, kFmtF16);   // [K; Q] . [S hi | S lo]
+constexpr uint32_t IDESC_N64 = idesc_f16(128, 64, false, true, kFmtF16);   // [K; Q] . S, M (TMEM) . R
+constexpr uint32_t IDESC_N32 = idesc_f16(128, 32, false, true, kFmtF16);   // M_lo (TMEM) . R_hi, A T . R_hi
 constexpr uint32_t IDESC_M = idesc_f16(128, 64, true, false, kFmtF16);     // K^T . T
-constexpr uint32_t IDESC_R = idesc_f16(128, 64, false, true, kFmtF16);     // M (TMEM) or A T . R
 
-// A bounded wait like tc::mbar_wait, but with the hardware's own suspension instead of a time hint: with
-// the hint a failed try sleeps in software, and each hand-over waits for the end of a sleep.
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+// A bounded wait like tc::mbar_wait.  A failed try suspends the warp for about 100 clocks in hardware, so
+// what a waiting warp issues in between is kept to a counter and a branch: at any time about half of the
+// warps wait, and with a C++ loop here they took half of the issue slots.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity, uint32_t tries) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, %3;\n"
+      "WAIT_%=:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra WAIT_%=;\n"
+      "DONE_%=:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(tries)
       : "memory");
   return ok != 0;
 }
 __device__ __noinline__ bool wait_retry(uint32_t bar, uint32_t parity, volatile int *abort, int *err) {
   const uint64_t t0 = globaltimer();
-  for (uint32_t i = 1;; ++i) {
-    if (try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0) {
-      if (*abort) return false;
-      if (globaltimer() - t0 > kWaitLimitNs) {
-        *abort = 1;
-        latch_error(err, (int)SSD_ERR_TIMEOUT);
-        return false;
-      }
+  while (!try_wait(bar, parity, 256)) {
+    if (*abort) return false;
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      latch_error(err, (int)SSD_ERR_TIMEOUT);
+      return false;
     }
   }
+  return true;
 }
 
 __device__ __forceinline__ uint64_t adv(uint64_t d, uint32_t bytes) {
@@ -130,44 +144,72 @@ __device__ __forceinline__ uint64_t adv(uint64_t d, uint32_t bytes) {
 __device__ __forceinline__ constexpr uint32_t kstep(int j) { return (j >> 2) * kHalf + (j & 3) * 32; }
 __device__ __forceinline__ constexpr uint32_t tstep(int j) { return (j >> 1) * 32 + (j & 1) * 8; }
 
-// The issuing loops stay rolled: an MMA runs for 32 to 64 clocks, and the chain's code should stay in
-// the instruction cache.
-__device__ __forceinline__ void issue_D1(uint32_t kq, uint32_t sbuf, uint32_t d) {
-  const uint64_t a = smem_desc_sw128(kq, 16, 1024), b = smem_desc_sw128(sbuf, kHalf, 1024);
-#pragma unroll 1
-  for (int j = 0; j < 8; ++j) mma_f16_ss(d, adv(a, kstep(j)), adv(b, j * 2048), IDESC_D1, j > 0);
+// The issuing warps run converged, one lane's instruction issuing the MMA: the descriptors then live in
+// uniform registers (issued from a divergent branch, their moves took 70 clocks per MMA).
+__device__ __forceinline__ void mma_ss(bool lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"((uint32_t)lead)
+      : "memory");
 }
-__device__ __forceinline__ void issue_M(uint32_t kq, uint32_t t, uint32_t d) {
+__device__ __forceinline__ void mma_ts(bool lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"((uint32_t)lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit(bool lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"((uint32_t)lead)
+      : "memory");
+}
+__device__ __forceinline__ void issue_D1(bool lead, uint32_t kq, uint32_t sbuf, uint32_t d) {
+  const uint64_t a = smem_desc_sw128(kq, 16, 1024), b = smem_desc_sw128(sbuf, 8192, 1024);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) mma_ss(lead, d, adv(a, kstep(j)), adv(b, j * 2048), IDESC_N64, j > 0);
+}
+__device__ __forceinline__ void issue_M(bool lead, uint32_t kq, uint32_t t, uint32_t d) {
   const uint64_t a = smem_desc_sw128(kq, kHalf, 1024), b = smem_desc_sw128(t, 16, 1024);
-#pragma unroll 1
+#pragma unroll
   for (int j = 0; j < 8; ++j)  // hi, then lo
-    mma_f16_ss(d, adv(a, (j & 3) * 2048), adv(b, (j >> 2) * 8192 + (j & 3) * 32), IDESC_M, j > 0);
+    mma_ss(lead, d, adv(a, (j & 3) * 2048), adv(b, (j >> 2) * 8192 + (j & 3) * 32), IDESC_M, j > 0);
 }
-// d = M_hi R~_hi + M_hi R~_lo + M_lo R~_hi  (64 tokens each)
-__device__ __forceinline__ void issue_S(uint32_t m, uint32_t r, uint32_t d) {
+// d = M_hi R_hi + M_lo R_hi | M_hi R_lo  (64 tokens)
+__device__ __forceinline__ void issue_S(bool lead, uint32_t m, uint32_t r, uint32_t d) {
   const uint64_t b = smem_desc_sw128(r, 8192, 1024);
-#pragma unroll 1
-  for (int j = 0; j < 12; ++j)
-    mma_f16_ts(d, m + tstep(j & 3) + (j >> 3) * 16, adv(b, 2048 * (j & 3) + (j >> 2 & 1) * 8192), IDESC_R, j > 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) mma_ts(lead, d, m + tstep(j), adv(b, 2048 * j), IDESC_N64, j > 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) mma_ts(lead, d, m + tstep(j) + 16, adv(b, 2048 * j), IDESC_N32, true);
 }
-// A T . R: rows 64-127 of the A operand are A T's; rows 0-63 are what lies 8 KB before it, and their
+// A T . R_hi: rows 64-127 of the A operand are A T's; rows 0-63 are what lies 8 KB before it, and their
 // results are not used
-__device__ __forceinline__ void issue_O(uint32_t at, uint32_t r, uint32_t d) {
+__device__ __forceinline__ void issue_O(bool lead, uint32_t at, uint32_t r, uint32_t d) {
   const uint64_t a = smem_desc_sw128(at - 8192, 16, 1024), b = smem_desc_sw128(r, 8192, 1024);
-#pragma unroll 1
-  for (int j = 0; j < 4; ++j) mma_f16_ss(d, adv(a, 32 * j), adv(b, 2048 * j), IDESC_R, j > 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) mma_ss(lead, d, adv(a, 32 * j), adv(b, 2048 * j), IDESC_N32, j > 0);
 }
 
 // Powers of two that bring a quantity bounded by m to [64, 128) and back.  Headroom: with alpha <= 1
 // and beta |k|^2 <= 2 the transition does not expand a state row s, so over a chunk
-// |s'| <= gamma |s| + 64 * 2 max|V|, and |R|, |R~| <= 2 (max|V| + |s|).  With m = gamma max|S_old| + max|V| that
+// |s'| <= gamma |s| + 64 * 2 max|V|, and |R| <= 2 (max|V| + |s|).  With m = gamma max|S_old| + max|V| that
 // is |S| <= (sqrt(128) + 128) m < 140 m and |R| < 282 max(m, max|V|): both below 65504 / 128 = 511.
 __device__ __forceinline__ float2 state_scale(float m) {
   const int e = min(max((int)((__float_as_uint(m) >> 23) & 255u), 8), 254);
   return make_float2(__uint_as_float((uint32_t)(260 - e) << 23), __uint_as_float((uint32_t)(e - 6) << 23));
 }
 
-__global__ void __launch_bounds__(kThreads, 1) ssd_delta_chunk_kernel(const DeltaPlan p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    ssd_delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_v, const DeltaPlan p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
@@ -183,13 +225,16 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_delta_chunk_kernel(const Delt
   uint32_t *misc = reinterpret_cast<uint32_t *>(smem + OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
   const auto wait = [&](int bar, uint32_t parity) {
-    return try_wait(BAR(bar), parity) || wait_retry(BAR(bar), parity, abort_flag, p.err);
+    return try_wait(BAR(bar), parity, 1024) || wait_retry(BAR(bar), parity, abort_flag, p.err);
   };
   const auto wait_buf = [&](int bar, int c) { return wait(bar + (c & 1), (c >> 1) & 1); };  // one of two copies
+  const auto wait_rec = [&](int bar, int c) { return wait(bar + c % kRecStages, (c / kRecStages) & 1); };  // of three
+  const auto tile_at = [&](int c) { return (uint32_t)(c & 1) * kTile; };
+  const auto rec_at = [&](int c) { return OFF_REC + (uint32_t)(c % kRecStages) * kRec; };
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(BAR(i), i == BAR_SREADY || i == BAR_RREADY ? 8 : i == BAR_MREADY || i == BAR_MREADY + 1 ? 4 : 1);
+      mbar_init(BAR(i), (i >= BAR_MREADY && i < BAR_D1) || i == BAR_RREADY || i == BAR_RREADY + 1 ? 4 : i / 2 == BAR_TEMPTY / 2 || (i >= BAR_REMPTY && i < BAR_READY) ? 2 : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -204,98 +249,117 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_delta_chunk_kernel(const Delt
   const int q4 = warp & 3;                           // TMEM lanes 32 q4 ..
   const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
 
-  if (warp == 12) {
-    // ------------------------------------------------------------------ MMAs of the chain
-    if (lane == 0) {
-      for (int c = 0; c < nck; ++c) {
-        const uint32_t stage = sb + (c & 1) * kStage;
-        if (!wait_buf(BAR_FULL, c) || !wait(BAR_SREADY, c & 1)) break;
-        tc_fence_after();
-        issue_D1(stage, sb + OFF_SB, tmem + TM_D1);
-        mma_commit(BAR(BAR_D1));
-        if (!wait_buf(BAR_MREADY, c) || !wait(BAR_RREADY, c & 1)) break;
-        tc_fence_after();
-        issue_S(tmem + TM_M + 64 * (c & 1), sb + OFF_RB, tmem + TM_S);
-        mma_commit(BAR(BAR_S));
-        issue_O(stage + OFF_AT, sb + OFF_RB + 16384, tmem + TM_O);
-        mma_commit(BAR(BAR_O));
-        mma_commit(BAR(BAR_EMPTY + (c & 1)));
-      }
-      mma_commit(BAR(BAR_DONE));  // no MMA may still be running when TMEM is released
-      int never_abort = 0;
-      mbar_wait(BAR(BAR_DONE), 0, &never_abort, p.err);
+  const bool lead = lane == 0;
+  if (warp == 12 || warp == 13) {
+    // ------------------------------------------------------------------ MMAs of a chain
+    const int half = warp - 12;
+    bool ok = true;
+    for (int c = 0; c < nck && ok; ++c) {
+      const uint32_t s_op = sb + OFF_SB + half * kHalf, r_op = sb + OFF_R + half * 8192;
+      ok = wait_rec(BAR_READY, c);
+      ok = wait(BAR_SREADY + half, c & 1) && ok;
+      tc_fence_after();
+      issue_D1(lead, sb + tile_at(c), s_op, tmem + TM_D1 + 64 * half);
+      commit(lead, BAR(BAR_D1 + half));
+      ok = wait_buf(BAR_MREADY, c) && ok;
+      ok = wait(BAR_RREADY + half, c & 1) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      issue_S(lead, tmem + TM_M + 64 * (c & 1), r_op, tmem + TM_S + 64 * half);
+      commit(lead, BAR(BAR_S + half));
+      issue_O(lead, sb + rec_at(c) + OFF_AT, r_op, tmem + TM_O + 32 * half);
+      commit(lead, BAR(BAR_O + half));
+      commit(lead, BAR(BAR_TEMPTY + (c & 1)));
+      commit(lead, BAR(BAR_REMPTY + c % kRecStages));
     }
-  } else if (warp == 13) {
+    commit(lead, BAR(BAR_DONE + half));  // no MMA may still be running when TMEM is released
+    int never_abort = 0;
+    mbar_wait(BAR(BAR_DONE + half), 0, &never_abort, p.err);
+    __syncwarp();
+  } else if (warp == 15) {
     // ------------------------------------------------------------------ MMAs of M
-    if (lane == 0) {
-      for (int c = 0; c < nck; ++c) {
-        // a loaded stage also says that the chain is through with the M of two chunks before
-        if (!wait_buf(BAR_FULL, c)) break;
-        tc_fence_after();
-        issue_M(sb + (c & 1) * kStage, sb + (c & 1) * kStage + OFF_T, tmem + TM_M + 64 * (c & 1));
-        mma_commit(BAR(BAR_M + (c & 1)));
-      }
-      mma_commit(BAR(BAR_DONE + 1));
-      int never_abort = 0;
-      mbar_wait(BAR(BAR_DONE + 1), 0, &never_abort, p.err);
+    bool ok = true;
+    for (int c = 0; c < nck && ok; ++c) {
+      // a loaded tile also says that the chains are through with the M of two chunks before
+      ok = wait_rec(BAR_READY, c);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      issue_M(lead, sb + tile_at(c), sb + rec_at(c) + OFF_T, tmem + TM_M + 64 * (c & 1));
+      commit(lead, BAR(BAR_M + (c & 1)));
     }
+    commit(lead, BAR(BAR_DONE + 2));
+    int never_abort = 0;
+    mbar_wait(BAR(BAR_DONE + 2), 0, &never_abort, p.err);
+    __syncwarp();
   } else if (warp == 14) {
-    // ------------------------------------------------------------------ loads
+    // ------------------------------------------------------------------ loads; the largest |V| of each chunk,
+    // times the largest |beta| / 2 where that is above one
     const long long ck0 = p.chunk0 ? p.chunk0[seq] : (long long)seq * nck;
-    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v) + base * p.vs + h * p.P + 64 * ph;
-    int c = 0;
-    for (; c < nck; ++c) {
-      const int rows = min(C, len - c * C);
-      const uint32_t dst = sb + (c & 1) * kStage, full = BAR(BAR_FULL + (c & 1));
-      bool ok = true;
-      if (lane == 0) {
-        ok = c < kStages || wait_buf(BAR_EMPTY, c - kStages);
-        if (ok) mbar_arrive_expect_tx(full, (uint32_t)(kDeltaTileBytes + kDeltaRecordBytes) + rows * 128);
+    const auto load_record = [&](int c) {  // and V
+      const uint32_t dst = sb + rec_at(c), full = BAR(BAR_RFULL + c % kRecStages);
+      if (c >= kRecStages && !wait_rec(BAR_REMPTY, c - kRecStages)) return false;
+      mbar_arrive_expect_tx(full, (uint32_t)kDeltaRecordBytes + 8192);
+      // 64 token rows, the ones after the sequence's end among them (they are not used)
+      tma_load_2d(dst + OFF_V, &tm_v, h * p.P + 64 * ph, (int)(base + c * C), full);
+      // V is the caller's; tiles and records are the front end's, which may still be running
+      // (programmatic dependent launch)
+      if (c == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+      bulk_load(dst, p.records + ((ck0 + c) * p.H + h) * kDeltaRecordBytes, (uint32_t)kDeltaRecordBytes, full);
+      return true;
+    };
+    const auto load_tile = [&](int c) {
+      const uint32_t full = BAR(BAR_TFULL + (c & 1));
+      if (c >= 2 && !wait_buf(BAR_TEMPTY, c - 2)) return false;
+      mbar_arrive_expect_tx(full, (uint32_t)kDeltaTileBytes);
+      bulk_load(sb + tile_at(c), p.tiles + ((ck0 + c) * p.G + h / p.hpg) * kDeltaTileBytes, (uint32_t)kDeltaTileBytes, full);
+      return true;
+    };
+    if (lead) prefetch_tmap(&tm_v);
+    int nr = 0, nt = 0;
+    bool ok = true;
+    for (int c = 0; c < nck; ++c) {
+      if (lead) {  // what chunk c - 2 has freed: the places of tile c and of record c + 1
+        while (ok && nr < min(nck, max(c + 2, kRecStages)) && (ok = load_record(nr))) ++nr;
+        while (ok && nt < min(nck, max(c + 1, 2)) && (ok = load_tile(nt))) ++nt;
       }
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      for (int r = lane; r < rows; r += 32) bulk_load(dst + OFF_V + r * kVPitch, v + (c * C + r) * p.vs, 128, full);
-      if (lane == 0) {
-        // V is the caller's; tiles and records are the front end's, which may still be running
-        // (programmatic dependent launch)
-        if (c == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-        bulk_load(dst, p.tiles + ((ck0 + c) * p.G + h / p.hpg) * kDeltaTileBytes, (uint32_t)kDeltaTileBytes, full);
-        bulk_load(dst + OFF_T, p.records + ((ck0 + c) * p.H + h) * kDeltaRecordBytes, (uint32_t)kDeltaRecordBytes, full);
-      }
-      __syncwarp();
-    }
-    if (lane == 0) {  // every load must land before the CTA may exit
-      int never_abort = 0;
-      for (int j = max(0, c - kStages); j < c; ++j) mbar_wait(BAR(BAR_FULL + (j & 1)), (j >> 1) & 1, &never_abort, p.err);
-    }
-  } else if (warp == 15) {
-    // ------------------------------------------------------------------ largest |V| of each chunk, times the
-    // largest |beta| / 2 where that is above one
-    for (int c = 0; c < nck; ++c) {
-      const bool ok = wait_buf(BAR_FULL, c);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const unsigned char *stage = smem + (c & 1) * kStage;
+      ok = wait_rec(BAR_RFULL, c);
+      ok = wait_buf(BAR_TFULL, c) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const unsigned char *stage = smem + rec_at(c);
       const int rows = min(C, len - c * C);
       uint32_t top = 0;
 #pragma unroll 4
       for (int r = lane >> 3; r < rows; r += 4) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(stage + OFF_V + r * kVPitch + (lane & 7) * 16);
+        const uint4 u = *reinterpret_cast<const uint4 *>(stage + OFF_V + r * 128 + (lane & 7) * 16);
         top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
                                      __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
       }
       top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
       const float2 b = reinterpret_cast<const float2 *>(stage + OFF_BETA)[lane];
       const uint32_t bt = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(b.x), fabsf(b.y))));
-      if (lane == 0) {
-        reinterpret_cast<float *>(smem + OFF_MAXV)[c & 1] = __uint_as_float(top << 16) * fmaxf(1.f, 0.5f * __uint_as_float(bt));
-        mbar_arrive(BAR(BAR_MAXV + (c & 1)));
+      if (lead) {
+        reinterpret_cast<float *>(smem + OFF_MAXV)[c % kRecStages] = __uint_as_float(top << 16) * fmaxf(1.f, 0.5f * __uint_as_float(bt));
+        mbar_arrive(BAR(BAR_READY + c % kRecStages));
       }
+      __syncwarp();
     }
+    if (lead) {  // every load must land before the CTA may exit
+      int never_abort = 0;
+      for (int k = max(0, nr - kRecStages); k < nr; ++k)
+        mbar_wait(BAR(BAR_RFULL + k % kRecStages), (k / kRecStages) & 1, &never_abort, p.err);
+      for (int k = max(0, nt - 2); k < nt; ++k) mbar_wait(BAR(BAR_TFULL + (k & 1)), (k >> 1) & 1, &never_abort, p.err);
+    }
+    __syncwarp();
   } else if (warp >= 8) {
-    // ------------------------------------------------------------------ M into its operand
+    // ------------------------------------------------------------------ M, its columns times
+    // rho_j 2^{cs_C - cs_j}, into its operand
     for (int c = 0; c < nck; ++c) {
       const bool ok = wait_buf(BAR_M, c);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
+      const float4 *f = reinterpret_cast<const float4 *>(smem + rec_at(c) + OFF_END);
 #pragma unroll 1
       for (int b = 0; b < 2; ++b) {
         const uint32_t at = tmem + TM_M + 64 * (c & 1) + 32 * b + lane_off;
@@ -304,7 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_delta_chunk_kernel(const Delt
         tmem_ld32(at, m);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) split2(make_float2(m[2 * j], m[2 * j + 1]), hv[j], lv[j]);
+        for (int j = 0; j < 8; ++j) {
+          const float4 x = f[8 * b + j];
+          split2(__fmul2_rn(make_float2(m[4 * j], m[4 * j + 1]), make_float2(x.x, x.y)), hv[2 * j], lv[2 * j]);
+          split2(__fmul2_rn(make_float2(m[4 * j + 2], m[4 * j + 3]), make_float2(x.z, x.w)), hv[2 * j + 1], lv[2 * j + 1]);
+        }
         tmem_st16(at, hv);
         tmem_st16(at + 16, lv);
       }
@@ -314,14 +382,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_delta_chunk_kernel(const Delt
       if (lane == 0) mbar_arrive(BAR(BAR_MREADY + (c & 1)));
     }
   } else {
-    // ------------------------------------------------------------------ the chain
-    const int hf = warp >> 2;                // state rows (columns of D1, S and O) 32 hf ..
+    // ------------------------------------------------------------------ the chains
+    const int hf = warp >> 2;                // half: state rows (columns of S and O) 32 hf ..
     const bool is_q = q4 >= 2;
     const int row = 32 * (q4 & 1) + lane;    // token of this thread's lane of D1 and O
     const int n = 32 * q4 + lane;            // state column of this thread
     const long long soff = (((long long)seq * p.H + h) * p.P + 64 * ph + 32 * hf) * kDState + n;
-    uint32_t *max_s = reinterpret_cast<uint32_t *>(smem + OFF_MAXS);
-    float2 S[16];
+    uint32_t *max_s = reinterpret_cast<uint32_t *>(smem + OFF_MAXS) + 8 * hf;
+    const uint32_t t_d1 = tmem + TM_D1 + 64 * hf, t_s = tmem + TM_S + 64 * hf, t_o = tmem + TM_O + 32 * hf;
+    float2 S[16];  // the state, times sc.x
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       S[i].x = p.h0 ? p.h0[soff + (2 * i) * kDState] : 0.f;
@@ -332,35 +401,60 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_delta_chunk_kernel(const Delt
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(fabsf(S[i].x), fabsf(S[i].y)));
       const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-      if (lane == 0) max_s[8 * buf + warp] = bits;
+      if (lane == 0) max_s[4 * buf + q4] = bits;
     };
     const auto read_max = [&](int buf) {
-      const uint4 a = *reinterpret_cast<const uint4 *>(max_s + 8 * buf), b = *reinterpret_cast<const uint4 *>(max_s + 8 * buf + 4);
-      return __uint_as_float(max(max(max(a.x, a.y), max(a.z, a.w)), max(max(b.x, b.y), max(b.z, b.w))));
+      const uint4 a = *reinterpret_cast<const uint4 *>(max_s + 4 * buf);
+      return __uint_as_float(max(max(a.x, a.y), max(a.z, a.w)));
     };
     publish_max(1);
-    named_bar(1, 256);
-    float m = read_max(1);  // bounds |S| as described at state_scale
-    float2 qs[16];          // 2^cs Q S^T of the chunk whose y is still to come
-    float back_o = 0.f, rho_q = 0.f;
+    named_bar(1 + hf, 128);
+    float m = read_max(1);  // bounds the state as described at state_scale
+    float2 sc = state_scale(m);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) S[i] = __fmul2_rn(S[i], make_float2(sc.x, sc.x));
+    // K rows: the chunk's V; Q rows: 2^cs Q S^T of the chunk whose y is still to come
+    float2 hold[16];
+    float gamma = 0.f, gamma_end = 0.f, beta = 0.f, rho = 0.f, vmax = 0.f;  // of the chunk
+    float back_o = 0.f, rho_y = 0.f;                                         // of the y to come
+    const auto load_rows = [&](int c) {
+      const unsigned char *stage = smem + rec_at(c);
+      const auto arr = [&](uint32_t off) { return reinterpret_cast<const float *>(stage + off); };
+      const bool ok = wait_rec(BAR_READY, c);
+      vmax = reinterpret_cast<const float *>(smem + OFF_MAXV)[c % kRecStages];
+      gamma = arr(OFF_GAMMA)[row];
+      gamma_end = arr(OFF_GAMMA)[C - 1];
+      rho = reinterpret_cast<const float *>(smem + tile_at(c) + (is_q ? OFF_RHOQ : OFF_RHOK))[row];
+      if (!is_q) {
+        const bool live = c * C + row < len;  // (the rows after may hold anything)
+        beta = live ? arr(OFF_BETA)[row] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 u = live ? *reinterpret_cast<const uint4 *>(stage + OFF_V + swz(row, 4 * hf + i)) : make_uint4(0, 0, 0, 0);
+          hold[2 * i] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+          hold[2 * i + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+        }
+      }
+      return ok;
+    };
     const auto put_y = [&](int c) {  // Q rows: y of chunk c
-      wait(BAR_O, c & 1);
+      wait(BAR_O + hf, c & 1);
       __syncwarp();
       tc_fence_after();
       const int t = c * C + row;
       const long long yo = (base + t) * p.ys + (long long)h * p.P + 64 * ph + 32 * hf;
       uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.y) + yo);
       const bool store = t < len && in_bounds(yo + 31, p.y_extent, p.err);
-      const float2 b2 = make_float2(back_o, back_o), r2 = make_float2(rho_q, rho_q);
+      const float2 b2 = make_float2(back_o, back_o), r2 = make_float2(rho_y, rho_y);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         float o[16];
-        tmem_ld16(tmem + TM_O + 32 * hf + 16 * x + lane_off, o);
+        tmem_ld16(t_o + 16 * x + lane_off, o);
         tmem_ld_wait();
         uint32_t u[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 f = __fmul2_rn(r2, __ffma2_rn(b2, make_float2(o[2 * i], o[2 * i + 1]), qs[8 * x + i]));
+          const float2 f = __fmul2_rn(r2, __ffma2_rn(b2, make_float2(o[2 * i], o[2 * i + 1]), hold[8 * x + i]));
           const __nv_bfloat162 v = __float22bfloat162_rn(f);
           u[i] = *reinterpret_cast<const uint32_t *>(&v);
         }
@@ -370,113 +464,97 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_delta_chunk_kernel(const Delt
         }
       }
     };
-    bool ok = true;
-    for (int c = 0;; ++c) {
-      const unsigned char *stage = smem + (c & 1) * kStage;
-      const auto arr = [&](uint32_t off) { return reinterpret_cast<const float *>(stage + off); };
-      const float2 sc = state_scale(m), sc2 = make_float2(sc.x, sc.x);
-      // S into its operand (after the last chunk too, where no product takes it)
+    bool ok = nck == 0 || load_rows(0);
+    for (int c = 0; c < nck; ++c) {
+      // S into its operand
+      unsigned char *so = smem + OFF_SB + hf * kHalf;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t hv[4], lv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split2(__fmul2_rn(S[4 * k + i], sc2), hv[i], lv[i]);
-        unsigned char *o = smem + OFF_SB + swz(n, 4 * hf + k);
-        *reinterpret_cast<uint4 *>(o) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-        *reinterpret_cast<uint4 *>(o + kHalf) = make_uint4(lv[0], lv[1], lv[2], lv[3]);
+        for (int i = 0; i < 4; ++i) split2(S[4 * k + i], hv[i], lv[i]);
+        *reinterpret_cast<uint4 *>(so + swz(n, k)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+        *reinterpret_cast<uint4 *>(so + swz(n, 4 + k)) = make_uint4(lv[0], lv[1], lv[2], lv[3]);
       }
       fence_proxy_async();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(BAR_SREADY));
-      // while K S^T runs: y of the chunk before, the bound of |S|, this chunk's rows
+      if (lead) mbar_arrive(BAR(BAR_SREADY + hf));
+      // while K S^T runs: y of the chunk before, the bound of |S|
       if (is_q && c > 0) put_y(c - 1);
-      if (c == nck) break;
       publish_max(c & 1);
-      ok = wait_buf(BAR_FULL, c);
-      ok = wait_buf(BAR_MAXV, c) && ok;
-      const float gamma = arr(OFF_GAMMA)[row] * sc.y, gamma_end = arr(OFF_GAMMA)[C - 1];
-      const float vmax = reinterpret_cast<const float *>(smem + OFF_MAXV)[c & 1];
       const float2 rsc = state_scale(fmaxf(m, vmax));
-      uint4 vv[4];
-      float b = 0.f, back_k = 0.f, to_end = 0.f;
-      if (!is_q) {
-        const bool live = c * C + row < len;
-        to_end = arr(OFF_END)[row];
-        if (live) b = arr(OFF_BETA)[row] * rsc.x;
-        back_k = -gamma * arr(OFF_RHOK)[row];
-        const uint4 *src = reinterpret_cast<const uint4 *>(stage + OFF_V + row * kVPitch + 64 * hf);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vv[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
-      } else {
-        rho_q = arr(OFF_RHOQ)[row];
-        back_o = rsc.y;
-      }
-      ok = wait(BAR_D1, c & 1) && ok;
+      rho_y = rho;
+      back_o = rsc.y;
+      const float g = gamma * sc.y, gk = -g * rho, b = beta * rsc.x;
+      const float2 g2 = make_float2(g, g), k2 = make_float2(gk, gk), b2 = make_float2(b, b);
+      ok = wait(BAR_D1 + hf, c & 1) && ok;
       __syncwarp();
       tc_fence_after();
-      const float2 g2 = make_float2(gamma, gamma), k2 = make_float2(back_k, back_k), b2 = make_float2(b, b);
-      const float2 e2 = make_float2(to_end, to_end);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         float d[16], e[16];
-        tmem_ld16(tmem + TM_D1 + 32 * hf + 16 * x + lane_off, d);
-        tmem_ld16(tmem + TM_D1 + 64 + 32 * hf + 16 * x + lane_off, e);
+        tmem_ld16(t_d1 + 16 * x + lane_off, d);
+        tmem_ld16(t_d1 + 32 + 16 * x + lane_off, e);
         tmem_ld_wait();
         if (is_q) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            qs[8 * x + i] = __fmul2_rn(g2, __fadd2_rn(make_float2(d[2 * i], d[2 * i + 1]), make_float2(e[2 * i], e[2 * i + 1])));
+            hold[8 * x + i] = __fmul2_rn(g2, __fadd2_rn(make_float2(d[2 * i], d[2 * i + 1]), make_float2(e[2 * i], e[2 * i + 1])));
         } else {
-          uint32_t hv[8], lv[8], rv[8];
+          uint32_t hv[8], lv[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint4 u4 = vv[2 * x + (i >> 2)];
-            const uint32_t u = (i & 3) == 0 ? u4.x : (i & 3) == 1 ? u4.y : (i & 3) == 2 ? u4.z : u4.w;
+            const float2 vp = hold[4 * x + i / 2];  // two bf16 pairs
+            const uint32_t u = __float_as_uint(i & 1 ? vp.y : vp.x);
             const float2 v = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
             const float2 ks = __fadd2_rn(make_float2(d[2 * i], d[2 * i + 1]), make_float2(e[2 * i], e[2 * i + 1]));
-            const float2 r = __fmul2_rn(b2, __ffma2_rn(k2, ks, v));
-            rv[i] = h2(__float22half2_rn(r));
-            split2(__fmul2_rn(e2, r), hv[i], lv[i]);
+            split2(__fmul2_rn(b2, __ffma2_rn(k2, ks, v)), hv[i], lv[i]);
           }
+          unsigned char *o = smem + OFF_R + hf * 8192;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            unsigned char *o = smem + OFF_RB + swz(row, 4 * hf + 2 * x + u);
-            *reinterpret_cast<uint4 *>(o) = make_uint4(hv[4 * u], hv[4 * u + 1], hv[4 * u + 2], hv[4 * u + 3]);
-            *reinterpret_cast<uint4 *>(o + 8192) = make_uint4(lv[4 * u], lv[4 * u + 1], lv[4 * u + 2], lv[4 * u + 3]);
-            *reinterpret_cast<uint4 *>(o + 16384) = make_uint4(rv[4 * u], rv[4 * u + 1], rv[4 * u + 2], rv[4 * u + 3]);
+            *reinterpret_cast<uint4 *>(o + swz(row, 2 * x + u)) = make_uint4(hv[4 * u], hv[4 * u + 1], hv[4 * u + 2], hv[4 * u + 3]);
+            *reinterpret_cast<uint4 *>(o + swz(row, 4 + 2 * x + u)) = make_uint4(lv[4 * u], lv[4 * u + 1], lv[4 * u + 2], lv[4 * u + 3]);
           }
         }
       }
       fence_proxy_async();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(BAR_RREADY));
-      // S = gamma_end S + M R~
-      const float2 ge = make_float2(gamma_end, gamma_end), y2 = make_float2(rsc.y, rsc.y);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) S[i] = __fmul2_rn(S[i], ge);
-      ok = wait(BAR_S, c & 1) && ok;
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
+      if (lead) mbar_arrive(BAR(BAR_RREADY + hf));
+      // S = gamma_end S + M R, in the next chunk's scale; while the product runs: the next chunk's rows
+      const float decay = gamma_end * sc.y, bound = vmax;
+      if (c + 1 < nck) ok = load_rows(c + 1) && ok;
+      ok = wait(BAR_S + hf, c & 1) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
       tc_fence_after();
-      m = fmaf(gamma_end, read_max(c & 1), vmax);
+      m = fmaf(decay, read_max(c & 1), bound);
+      sc = state_scale(m);
+      const float ge = decay * sc.x, yn = rsc.y * sc.x;
+      const float2 ge2 = make_float2(ge, ge), y2 = make_float2(yn, yn);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) S[i] = __fmul2_rn(S[i], ge2);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float d[16];
-        tmem_ld16(tmem + TM_S + 32 * hf + 16 * x + lane_off, d);
+        float d[16], e[16];
+        tmem_ld16(t_s + 16 * x + lane_off, d);
+        tmem_ld16(t_s + 32 + 16 * x + lane_off, e);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) S[8 * x + i] = __ffma2_rn(y2, make_float2(d[2 * i], d[2 * i + 1]), S[8 * x + i]);
+        for (int i = 0; i < 8; ++i)
+          S[8 * x + i] = __ffma2_rn(y2, __fadd2_rn(make_float2(d[2 * i], d[2 * i + 1]), make_float2(e[2 * i], e[2 * i + 1])), S[8 * x + i]);
       }
     }
-    if (ok && p.h_final) {
+    if (ok) {
+      if (is_q && nck > 0) put_y(nck - 1);
+      if (p.h_final) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (in_bounds(soff + (long long)i * kDState, p.state_extent, p.err))
-          p.h_final[soff + (long long)i * kDState] = i & 1 ? S[i / 2].y : S[i / 2].x;
+        for (int i = 0; i < 32; ++i)
+          if (in_bounds(soff + (long long)i * kDState, p.state_extent, p.err))
+            p.h_final[soff + (long long)i * kDState] = sc.y * (i & 1 ? S[i / 2].y : S[i / 2].x);
+      }
     }
   }
 
@@ -489,9 +567,32 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_delta_chunk_kernel(const Delt
 #undef BAR
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
 }  // namespace
 
 cudaError_t launch_delta_chunks(const DeltaPlan &p, cudaStream_t s) {
+  // V as one matrix of all token rows; a box is 64 rows of 64 state rows
+  const auto encode = encode_fn();
+  if (!encode) return cudaErrorNotSupported;
+  CUtensorMap tm;
+  const cuuint64_t dims[2] = {(cuuint64_t)p.H * p.P, (cuuint64_t)p.rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)p.vs * 2};
+  const cuuint32_t box[2] = {64, C}, ones[2] = {1, 1};
+  if (encode(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p.v), dims, strides, box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   cudaError_t e = set_smem_attr(ssd_delta_chunk_kernel, kSmem, s);
   if (e != cudaSuccess) return e;
   // a programmatic dependent of the front end: its set-up and first loads of V overlap the front
@@ -506,7 +607,7 @@ cudaError_t launch_delta_chunks(const DeltaPlan &p, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
   lc.numAttrs = 1;
-  e = cudaLaunchKernelEx(&lc, ssd_delta_chunk_kernel, p);
+  e = cudaLaunchKernelEx(&lc, ssd_delta_chunk_kernel, tm, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
