@@ -27,12 +27,11 @@
 // beside it) is rounded to 11 bits: y is then rounded to bf16's 8.
 //
 // Roles (16 warps, so that a thread may have 128 registers).  Warps 0-7, the chain: S into its operand, R
-// from K S^T, the new S, y.  Their two halves, 32 state rows each, are chains of their own, so that the
-// conversions of the one run beside the products of the other.  Warps 8-11 bring M (of the chunk
-// after) into its operand.  Warps 12 and 13 issue the MMAs of the two chains, warp 15 those of M, warp
-// 14 loads (TMA tiles of V, bulk copies of the front end's tiles and records) and finds the largest |V|
-// of each chunk.  Hand-overs are mbarriers; every wait is bounded: a timeout makes every role leave and
-// latches SSD_ERR_TIMEOUT.
+// from K S^T, the new S, y.  Their two halves, 32 state rows each, are chains of their own, one
+// product apart, so that the conversions of the one run beside the products of the other.  Warps 8-11 bring M
+// (of the chunk after) into its operand.  Warp 12 issues the MMAs of the chains, warp 13 those of M, warp
+// 14 loads, warp 15 loads T and finds the largest |V| of each chunk.  Hand-overs are mbarriers; every
+// wait is bounded: a timeout makes every role leave and latches SSD_ERR_TIMEOUT.
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
@@ -50,49 +49,52 @@ using namespace delta;
 constexpr int C = kDeltaChunk;
 constexpr int kThreads = 16 * 32;
 constexpr uint32_t kHalf = 16384;  // 128 rows x 128 bytes
-// Two rings of stages: the group's tile (from L2, as a rule: 16 heads or so share it), two deep, and the
-// head's record and V, three deep, since a load takes about as long as a chunk.
+// Rings of what is loaded, as deep as it is needed early: the group's tile (K and Q; M takes K a chunk ahead of
+// the chain, and a load takes more than half a chunk) three, T two (M alone takes it), A T two, V
+// with the head's gates three.
+constexpr int kDeep = 3;
 constexpr uint32_t OFF_RHOK = 2 * kHalf;          // the tile's row factors follow its operands
 constexpr uint32_t OFF_RHOQ = OFF_RHOK + 256;
 constexpr uint32_t kTile = 33 * 1024;
-constexpr int kRecStages = 3;
-constexpr uint32_t OFF_T = 0;                     // the record: T~^T hi, lo, A T; three arrays of 64 floats
-constexpr uint32_t OFF_AT = 2 * 8192;
-constexpr uint32_t OFF_BETA = 3 * 8192;
+static_assert(OFF_RHOQ + 256 == kDeltaTileBytes && kDeltaTileBytes <= kTile, "as loaded");
+constexpr uint32_t kT = 16384, kAT = 8192;        // T~^T hi, lo; A T
+constexpr uint32_t OFF_BETA = 8192;               // after V (64 rows of 128 bytes, swizzled): three arrays of 64 floats
 constexpr uint32_t OFF_GAMMA = OFF_BETA + 256;
 constexpr uint32_t OFF_END = OFF_GAMMA + 256;
-constexpr uint32_t OFF_V = (OFF_END + 256 + 1023) / 1024 * 1024;  // 64 rows of 128 bytes, swizzled
-constexpr uint32_t kRec = OFF_V + 8192;
-static_assert(OFF_RHOQ + 256 == kDeltaTileBytes && kDeltaTileBytes <= kTile && OFF_END + 256 == kDeltaRecordBytes, "as loaded");
+constexpr uint32_t kVG = 9 * 1024;
+static_assert(kT + kAT + 3 * 256 == kDeltaRecordBytes && OFF_END + 256 <= kVG, "as loaded");
 // CTA
-constexpr uint32_t OFF_REC = 2 * kTile;
-constexpr uint32_t OFF_SB = OFF_REC + kRecStages * kRec;  // S operands of the halves: [n][32 p hi, 32 p lo], 128 rows each
+constexpr uint32_t OFF_T = kDeep * kTile;
+constexpr uint32_t OFF_AT = OFF_T + 2 * kT;
+constexpr uint32_t OFF_VG = OFF_AT + 2 * kAT;
+constexpr uint32_t OFF_SB = OFF_VG + kDeep * kVG;  // S operands of the halves: [n][32 p hi, 32 p lo], 128 rows each
 constexpr uint32_t OFF_R = OFF_SB + 2 * kHalf;    // R operands of the halves: [token][32 p hi, 32 p lo], 64 rows each
 constexpr uint32_t OFF_MAXS = OFF_R + 2 * 8192;      // largest |S| per chain warp, two chunks
-constexpr uint32_t OFF_MAXV = OFF_MAXS + 64;      // bound of what the chunk adds, per record stage
+constexpr uint32_t OFF_MAXV = OFF_MAXS + 64;      // bound of what the chunk adds, per place in the ring
 constexpr uint32_t OFF_BAR = OFF_MAXV + 64;
 // A barrier that can complete again before every waiter has seen the phase before has one copy per
 // buffer, so that a parity test never sees two phases at once.
 enum {
-  BAR_TFULL,                       // [2] tile loaded
-  BAR_TEMPTY = BAR_TFULL + 2,      // [2] its last products, and those of its M, are done (2 issuers)
-  BAR_RFULL = BAR_TEMPTY + 2,      // [3] record and V loaded
-  BAR_REMPTY = BAR_RFULL + kRecStages,   // [3] released as the tile (2 issuers)
-  BAR_READY = BAR_REMPTY + kRecStages,   // [3] record, V and tile loaded, and the bound of what the chunk adds known
-  BAR_M = BAR_READY + kRecStages,   // [2] M done
+  BAR_TILE,                        // [3] tile loaded
+  BAR_VG = BAR_TILE + kDeep,       // [3] V and gates loaded
+  BAR_READY = BAR_VG + kDeep,      // [3] both, and the bound of what the chunk adds known
+  BAR_EMPTY = BAR_READY + kDeep,   // [3] the chunk's last product (and every read before it) is done
+  BAR_T = BAR_EMPTY + kDeep,       // [2] T loaded
+  BAR_AT = BAR_T + 2,              // [2] A T loaded
+  BAR_M = BAR_AT + 2,              // [2] M done
   BAR_MREADY = BAR_M + 2,          // [2] M operand in tensor memory (4 warps)
   BAR_SREADY = BAR_MREADY + 2,     // [2 halves] S operand written (4 warps)
-  BAR_D1 = BAR_SREADY + 2,         // [2 halves] K S^T, Q S^T done
-  BAR_RREADY = BAR_D1 + 2,         // [2 halves] R operand written, D1 read (4 warps)
-  BAR_S = BAR_RREADY + 2,          // [2 halves] M R done
+  BAR_RREADY = BAR_SREADY + 2,     // [2 halves] R operand written, D1 read (4 warps)
+  BAR_D1 = BAR_RREADY + 2,         // [2 halves] K S^T, Q S^T done
+  BAR_S = BAR_D1 + 2,              // [2 halves] M R done
   BAR_O = BAR_S + 2,               // [2 halves] A T R done
-  BAR_DONE = BAR_O + 2,            // [3] nothing of an issuer's left in flight
-  kNumBars = BAR_DONE + 3
+  BAR_DONE = BAR_O + 2,            // [2] nothing of an issuer's left in flight
+  kNumBars = BAR_DONE + 2
 };
-constexpr uint32_t OFF_MISC = OFF_BAR + 8 * 32;   // [0] TMEM base, [1] abort flag
+constexpr uint32_t OFF_MISC = OFF_BAR + 8 * 32;   // [0] TMEM base, [1] abort flag, [2] the same for the last waits
 constexpr uint32_t kSmem = OFF_MISC + 16 + 1024;  // room to align the base to 1024 bytes
 static_assert(kNumBars <= 32 && kSmem <= 232448, "shared memory");
-static_assert(OFF_SB % 1024 == 0 && OFF_R % 1024 == 0 && OFF_T % 1024 == 0, "swizzle alignment");
+static_assert(OFF_SB % 1024 == 0 && OFF_R % 1024 == 0 && OFF_T % 1024 == 0 && OFF_VG % 1024 == 0, "swizzle alignment");
 
 // TMEM columns.  K rows are lanes 0-63 of D1, Q rows lanes 64-127, as are the rows of A T R (lanes 0-63
 // of it are never used).  D1 and S have per half 32 columns of the products with hi, 32 of those with
@@ -104,99 +106,117 @@ constexpr uint32_t IDESC_N64 = idesc_f16(128, 64, false, true, kFmtF16);   // [K
 constexpr uint32_t IDESC_N32 = idesc_f16(128, 32, false, true, kFmtF16);   // M_lo (TMEM) . R_hi, A T . R_hi
 constexpr uint32_t IDESC_M = idesc_f16(128, 64, true, false, kFmtF16);     // K^T . T
 
-// A bounded wait like tc::mbar_wait.  A failed try suspends the warp for about 100 clocks in hardware, so
-// what a waiting warp issues in between is kept to a counter and a branch: at any time about half of the
-// warps wait, and with a C++ loop here they took half of the issue slots.
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity, uint32_t tries) {
+// A bounded wait.  A try suspends the warp for a while in hardware; after every 256 the abort flag is
+// looked at, and after 2^17 times that (about a second) the flag is set to 2.  In one piece of
+// assembly, because a warp that waits should issue little (about half of them wait at any time), and
+// because every wait of every role sits in the instruction cache.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint32_t abort) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, %3;\n"
-      "WAIT_%=:\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n, m, f;\n\t"
+      "mov.u32 m, 131072;\n"
+      "OUTER_%=:\n\t"
+      "mov.u32 n, 256;\n"
+      "TRY_%=:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "@p bra DONE_%=;\n\t"
       "sub.u32 n, n, 1;\n\t"
       "setp.ne.u32 q, n, 0;\n\t"
-      "@q bra WAIT_%=;\n"
+      "@q bra TRY_%=;\n\t"
+      "ld.volatile.shared.u32 f, [%3];\n\t"
+      "setp.ne.u32 q, f, 0;\n\t"
+      "@q bra DONE_%=;\n\t"
+      "sub.u32 m, m, 1;\n\t"
+      "setp.ne.u32 q, m, 0;\n\t"
+      "@q bra OUTER_%=;\n\t"
+      "st.volatile.shared.u32 [%3], 2;\n"
       "DONE_%=:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(tries)
+      : "r"(bar), "r"(parity), "r"(abort)
       : "memory");
   return ok != 0;
 }
-__device__ __noinline__ bool wait_retry(uint32_t bar, uint32_t parity, volatile int *abort, int *err) {
-  const uint64_t t0 = globaltimer();
-  while (!try_wait(bar, parity, 256)) {
-    if (*abort) return false;
-    if (globaltimer() - t0 > kWaitLimitNs) {
-      *abort = 1;
-      latch_error(err, (int)SSD_ERR_TIMEOUT);
-      return false;
+
+// Position in a ring of D places: the place, and the parity of its current use
+template <int D>
+struct Ring {
+  int at = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == D) {
+      at = 0;
+      parity ^= 1;
     }
   }
-  return true;
-}
+};
 
-__device__ __forceinline__ uint64_t adv(uint64_t d, uint32_t bytes) {
-  return (d & 0xFFFFFFFF00000000ull) | (static_cast<uint32_t>(d) + (bytes >> 4));
-}
-__device__ __forceinline__ constexpr uint32_t kstep(int j) { return (j >> 2) * kHalf + (j & 3) * 32; }
+// Start address field of an operand's descriptor, advanced by adding to it (16-byte units; every operand lies
+// below 256 KB); the other word holds the strides, the version bits and the 128-byte swizzle.
+__device__ __forceinline__ uint32_t op_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | (lbo >> 4) << 16; }
+constexpr uint32_t kOpHi = 1024 >> 4 | 1u << 14 | 2u << 29;
+__device__ __forceinline__ constexpr uint32_t kstep(int j) { return ((j >> 2) * kHalf + (j & 3) * 32) >> 4; }
 __device__ __forceinline__ constexpr uint32_t tstep(int j) { return (j >> 1) * 32 + (j & 1) * 8; }
 
-// The issuing warps run converged, one lane's instruction issuing the MMA: the descriptors then live in
-// uniform registers (issued from a divergent branch, their moves took 70 clocks per MMA).
-__device__ __forceinline__ void mma_ss(bool lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// The issuing warps run converged and elect a lane per instruction, and what the descriptors come from is
+// broadcast with shuffles: the compiler then knows it to be uniform and keeps the descriptors in uniform
+// registers.  Moved there from a divergent branch for every MMA, they cost 50 to 80 clocks each, more
+// than the MMA (SS N = 64: 49 clocks, its operands' shared-memory reads; TS N = 64: 32, N = 32: 16).
+template <uint32_t kIdesc>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %5};\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"((uint32_t)lead)
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "n"(kIdesc), "r"((uint32_t)acc), "n"(kOpHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(bool lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+template <uint32_t kIdesc>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"((uint32_t)lead)
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "n"(kIdesc), "r"((uint32_t)acc), "n"(kOpHi)
       : "memory");
 }
-__device__ __forceinline__ void commit(bool lead, uint32_t bar) {
+__device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-      "r"((uint32_t)lead)
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void issue_D1(bool lead, uint32_t kq, uint32_t sbuf, uint32_t d) {
-  const uint64_t a = smem_desc_sw128(kq, 16, 1024), b = smem_desc_sw128(sbuf, 8192, 1024);
+__device__ __forceinline__ void issue_D1(uint32_t kq, uint32_t sbuf, uint32_t d) {
+  const uint32_t a = op_lo(kq, 16), b = op_lo(sbuf, 8192);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) mma_ss(lead, d, adv(a, kstep(j)), adv(b, j * 2048), IDESC_N64, j > 0);
+  for (int j = 0; j < 8; ++j) mma_ss<IDESC_N64>(d, a + kstep(j), b + j * 128, j > 0);
 }
-__device__ __forceinline__ void issue_M(bool lead, uint32_t kq, uint32_t t, uint32_t d) {
-  const uint64_t a = smem_desc_sw128(kq, kHalf, 1024), b = smem_desc_sw128(t, 16, 1024);
+__device__ __forceinline__ void issue_M(uint32_t kq, uint32_t t, uint32_t d) {
+  const uint32_t a = op_lo(kq, kHalf), b = op_lo(t, 16);
 #pragma unroll
   for (int j = 0; j < 8; ++j)  // hi, then lo
-    mma_ss(lead, d, adv(a, (j & 3) * 2048), adv(b, (j >> 2) * 8192 + (j & 3) * 32), IDESC_M, j > 0);
+    mma_ss<IDESC_M>(d, a + (j & 3) * 128, b + (j >> 2) * 512 + (j & 3) * 2, j > 0);
 }
 // d = M_hi R_hi + M_lo R_hi | M_hi R_lo  (64 tokens)
-__device__ __forceinline__ void issue_S(bool lead, uint32_t m, uint32_t r, uint32_t d) {
-  const uint64_t b = smem_desc_sw128(r, 8192, 1024);
+__device__ __forceinline__ void issue_S(uint32_t m, uint32_t r, uint32_t d) {
+  const uint32_t b = op_lo(r, 8192);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) mma_ts(lead, d, m + tstep(j), adv(b, 2048 * j), IDESC_N64, j > 0);
+  for (int j = 0; j < 4; ++j) mma_ts<IDESC_N64>(d, m + tstep(j), b + 128 * j, j > 0);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) mma_ts(lead, d, m + tstep(j) + 16, adv(b, 2048 * j), IDESC_N32, true);
+  for (int j = 0; j < 4; ++j) mma_ts<IDESC_N32>(d, m + tstep(j) + 16, b + 128 * j, true);
 }
 // A T . R_hi: rows 64-127 of the A operand are A T's; rows 0-63 are what lies 8 KB before it, and their
 // results are not used
-__device__ __forceinline__ void issue_O(bool lead, uint32_t at, uint32_t r, uint32_t d) {
-  const uint64_t a = smem_desc_sw128(at - 8192, 16, 1024), b = smem_desc_sw128(r, 8192, 1024);
+__device__ __forceinline__ void issue_O(uint32_t at, uint32_t r, uint32_t d) {
+  const uint32_t a = op_lo(at - 8192, 16), b = op_lo(r, 8192);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) mma_ss(lead, d, adv(a, 32 * j), adv(b, 2048 * j), IDESC_N32, j > 0);
+  for (int j = 0; j < 4; ++j) mma_ss<IDESC_N32>(d, a + 2 * j, b + 128 * j, j > 0);
 }
 
 // Powers of two that bring a quantity bounded by m to [64, 128) and back.  Headroom: with alpha <= 1
@@ -212,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ssd_delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_v, const DeltaPlan p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const uint32_t sb = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sb = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int halves = p.P >> 6;
   const int h = blockIdx.x / halves, ph = blockIdx.x % halves;
   const int seq = p.order ? p.order[blockIdx.y] : (int)blockIdx.y;
@@ -223,143 +243,183 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar0 = sb + OFF_BAR;
 #define BAR(i) (bar0 + 8u * (uint32_t)(i))
   uint32_t *misc = reinterpret_cast<uint32_t *>(smem + OFF_MISC);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
-  const auto wait = [&](int bar, uint32_t parity) {
-    return try_wait(BAR(bar), parity, 1024) || wait_retry(BAR(bar), parity, abort_flag, p.err);
-  };
-  const auto wait_buf = [&](int bar, int c) { return wait(bar + (c & 1), (c >> 1) & 1); };  // one of two copies
-  const auto wait_rec = [&](int bar, int c) { return wait(bar + c % kRecStages, (c / kRecStages) & 1); };  // of three
-  const auto tile_at = [&](int c) { return (uint32_t)(c & 1) * kTile; };
-  const auto rec_at = [&](int c) { return OFF_REC + (uint32_t)(c % kRecStages) * kRec; };
+  const uint32_t abort_at = sb + OFF_MISC + 4;
+  const auto wait = [&](int bar, uint32_t parity) { return wait_bounded(BAR(bar), parity, abort_at); };
+  // before leaving, whatever the abort flag says
+  const auto settle = [&](int bar, uint32_t parity) { wait_bounded(BAR(bar), parity, abort_at + 4); };
+  const auto wait2 = [&](int bar, int c) { return wait(bar + (c & 1), (c >> 1) & 1); };  // one of two copies
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(BAR(i), (i >= BAR_MREADY && i < BAR_D1) || i == BAR_RREADY || i == BAR_RREADY + 1 ? 4 : i / 2 == BAR_TEMPTY / 2 || (i >= BAR_REMPTY && i < BAR_READY) ? 2 : 1);
-    *abort_flag = 0;
+      mbar_init(BAR(i), i >= BAR_MREADY && i < BAR_D1 ? 4 : 1);
+    misc[1] = misc[2] = 0;
     fence_mbar_init();
   }
-  if (warp == 15) {
+  if (warp == 13) {
     tmem_alloc(sb + OFF_MISC, TM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = misc[0];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
   const int q4 = warp & 3;                           // TMEM lanes 32 q4 ..
   const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
 
   const bool lead = lane == 0;
-  if (warp == 12 || warp == 13) {
-    // ------------------------------------------------------------------ MMAs of a chain
-    const int half = warp - 12;
+  if (warp == 12) {
+    // ------------------------------------------------------------------ MMAs of the chains, one half's after the
+    // other's: while those of one run, the other converts
+    Ring<kDeep> r;
     bool ok = true;
-    for (int c = 0; c < nck && ok; ++c) {
-      const uint32_t s_op = sb + OFF_SB + half * kHalf, r_op = sb + OFF_R + half * 8192;
-      ok = wait_rec(BAR_READY, c);
-      ok = wait(BAR_SREADY + half, c & 1) && ok;
-      tc_fence_after();
-      issue_D1(lead, sb + tile_at(c), s_op, tmem + TM_D1 + 64 * half);
-      commit(lead, BAR(BAR_D1 + half));
-      ok = wait_buf(BAR_MREADY, c) && ok;
-      ok = wait(BAR_RREADY + half, c & 1) && ok;
+    for (int c = 0; c < nck && ok; ++c, r.next()) {
+      ok = wait(BAR_READY + r.at, r.parity);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        ok = wait(BAR_SREADY + half, c & 1) && ok;
+        tc_fence_after();
+        issue_D1(sb + r.at * kTile, sb + OFF_SB + half * kHalf, tmem + TM_D1 + 64 * half);
+        commit(BAR(BAR_D1 + half));
+      }
+      ok = wait2(BAR_MREADY, c) && ok;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        ok = wait(BAR_RREADY + half, c & 1) && ok;
+        tc_fence_after();
+        issue_S(tmem + TM_M + 64 * (c & 1), sb + OFF_R + half * 8192, tmem + TM_S + 64 * half);
+        commit(BAR(BAR_S + half));
+      }
+      ok = wait2(BAR_AT, c) && ok;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        issue_O(sb + OFF_AT + (c & 1) * kAT, sb + OFF_R + half * 8192, tmem + TM_O + 32 * half);
+        commit(BAR(BAR_O + half));
+      }
+      commit(BAR(BAR_EMPTY + r.at));
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    commit(BAR(BAR_DONE));  // no MMA may still be running when TMEM is released
+    settle(BAR_DONE, 0);
+  } else if (warp == 13) {
+    // ------------------------------------------------------------------ MMAs of M
+    Ring<kDeep> r, e;
+    bool ok = true;
+    for (int c = 0; c < nck && ok; ++c, r.next()) {
+      ok = wait(BAR_TILE + r.at, r.parity);
+      ok = wait2(BAR_T, c) && ok;
+      if (c >= 2) {  // the M of two chunks before is read
+        ok = wait(BAR_EMPTY + e.at, e.parity) && ok;
+        e.next();
+      }
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      issue_S(lead, tmem + TM_M + 64 * (c & 1), r_op, tmem + TM_S + 64 * half);
-      commit(lead, BAR(BAR_S + half));
-      issue_O(lead, sb + rec_at(c) + OFF_AT, r_op, tmem + TM_O + 32 * half);
-      commit(lead, BAR(BAR_O + half));
-      commit(lead, BAR(BAR_TEMPTY + (c & 1)));
-      commit(lead, BAR(BAR_REMPTY + c % kRecStages));
+      issue_M(sb + r.at * kTile, sb + OFF_T + (c & 1) * kT, tmem + TM_M + 64 * (c & 1));
+      commit(BAR(BAR_M + (c & 1)));
     }
-    commit(lead, BAR(BAR_DONE + half));  // no MMA may still be running when TMEM is released
-    int never_abort = 0;
-    mbar_wait(BAR(BAR_DONE + half), 0, &never_abort, p.err);
+    commit(BAR(BAR_DONE + 1));
+    settle(BAR_DONE + 1, 0);
+  } else if (warp == 14) {
+    // ------------------------------------------------------------------ loads of tiles, V, gates, A T
+    if (lead) {
+      prefetch_tmap(&tm_v);
+      const long long ck0 = p.chunk0 ? p.chunk0[seq] : (long long)seq * nck;
+      const unsigned char *rec = p.records + (ck0 * p.H + h) * kDeltaRecordBytes + kT;
+      const unsigned char *tile = p.tiles + (ck0 * p.G + h / p.hpg) * kDeltaTileBytes;
+      const long long rec_step = p.H * kDeltaRecordBytes, tile_step = p.G * kDeltaTileBytes;
+      Ring<kDeep> r, e;  // to load; to become free
+      int n = 0, n_at = 0;
+      // Turn c: tile, V and gates of chunk c, into the place of chunk c - 3; A T of chunk c - 1 (and in
+      // turn 0 of chunk 0), whose two places are free then too.  The last turn loads A T alone.
+      for (int c = 0; c <= nck; ++c) {
+        if (c >= kDeep) {
+          if (!wait(BAR_EMPTY + e.at, e.parity)) break;
+          e.next();
+        }
+        if (c < nck) {
+          const uint32_t vg = BAR(BAR_VG + r.at), tb = BAR(BAR_TILE + r.at), dst = sb + OFF_VG + r.at * kVG;
+          mbar_arrive_expect_tx(vg, 8192 + 768);
+          // 64 token rows, the ones after the sequence's end among them (they are not used)
+          tma_load_2d(dst, &tm_v, h * p.P + 64 * ph, (int)(base + c * C), vg);
+          // V is the caller's; tiles and records are the front end's, which may still be running
+          // (programmatic dependent launch)
+          if (c == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+          mbar_arrive_expect_tx(tb, (uint32_t)kDeltaTileBytes);
+          bulk_load(sb + r.at * kTile, tile + c * tile_step, (uint32_t)kDeltaTileBytes, tb);
+          bulk_load(dst + OFF_BETA, rec + c * rec_step + kAT, 768, vg);
+          r.next();
+          ++n;
+        }
+        if (c != 1 && n_at < nck) {
+          const uint32_t at = BAR(BAR_AT + (n_at & 1));
+          mbar_arrive_expect_tx(at, kAT);
+          bulk_load(sb + OFF_AT + (n_at & 1) * kAT, rec + n_at * rec_step, kAT, at);
+          ++n_at;
+        }
+      }
+      // every load must land before the CTA may exit
+      for (int k = 0; k < kDeep; ++k)
+        if (k < n) {
+          const uint32_t last = k < r.at ? r.parity : r.parity ^ 1;
+          settle(BAR_VG + k, last);
+          settle(BAR_TILE + k, last);
+        }
+      for (int k = max(0, n_at - 2); k < n_at; ++k) settle(BAR_AT + (k & 1), (k >> 1) & 1);
+    }
     __syncwarp();
   } else if (warp == 15) {
-    // ------------------------------------------------------------------ MMAs of M
-    bool ok = true;
-    for (int c = 0; c < nck && ok; ++c) {
-      // a loaded tile also says that the chains are through with the M of two chunks before
-      ok = wait_rec(BAR_READY, c);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-      issue_M(lead, sb + tile_at(c), sb + rec_at(c) + OFF_T, tmem + TM_M + 64 * (c & 1));
-      commit(lead, BAR(BAR_M + (c & 1)));
-    }
-    commit(lead, BAR(BAR_DONE + 2));
-    int never_abort = 0;
-    mbar_wait(BAR(BAR_DONE + 2), 0, &never_abort, p.err);
-    __syncwarp();
-  } else if (warp == 14) {
-    // ------------------------------------------------------------------ loads; the largest |V| of each chunk,
+    // ------------------------------------------------------------------ loads of T; the largest |V| of each chunk,
     // times the largest |beta| / 2 where that is above one
     const long long ck0 = p.chunk0 ? p.chunk0[seq] : (long long)seq * nck;
-    const auto load_record = [&](int c) {  // and V
-      const uint32_t dst = sb + rec_at(c), full = BAR(BAR_RFULL + c % kRecStages);
-      if (c >= kRecStages && !wait_rec(BAR_REMPTY, c - kRecStages)) return false;
-      mbar_arrive_expect_tx(full, (uint32_t)kDeltaRecordBytes + 8192);
-      // 64 token rows, the ones after the sequence's end among them (they are not used)
-      tma_load_2d(dst + OFF_V, &tm_v, h * p.P + 64 * ph, (int)(base + c * C), full);
-      // V is the caller's; tiles and records are the front end's, which may still be running
-      // (programmatic dependent launch)
-      if (c == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-      bulk_load(dst, p.records + ((ck0 + c) * p.H + h) * kDeltaRecordBytes, (uint32_t)kDeltaRecordBytes, full);
-      return true;
-    };
-    const auto load_tile = [&](int c) {
-      const uint32_t full = BAR(BAR_TFULL + (c & 1));
-      if (c >= 2 && !wait_buf(BAR_TEMPTY, c - 2)) return false;
-      mbar_arrive_expect_tx(full, (uint32_t)kDeltaTileBytes);
-      bulk_load(sb + tile_at(c), p.tiles + ((ck0 + c) * p.G + h / p.hpg) * kDeltaTileBytes, (uint32_t)kDeltaTileBytes, full);
-      return true;
-    };
-    if (lead) prefetch_tmap(&tm_v);
-    int nr = 0, nt = 0;
-    bool ok = true;
-    for (int c = 0; c < nck; ++c) {
-      if (lead) {  // what chunk c - 2 has freed: the places of tile c and of record c + 1
-        while (ok && nr < min(nck, max(c + 2, kRecStages)) && (ok = load_record(nr))) ++nr;
-        while (ok && nt < min(nck, max(c + 1, 2)) && (ok = load_tile(nt))) ++nt;
-      }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      ok = wait_rec(BAR_RFULL, c);
-      ok = wait_buf(BAR_TFULL, c) && ok;
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const unsigned char *stage = smem + rec_at(c);
-      const int rows = min(C, len - c * C);
-      uint32_t top = 0;
+    const unsigned char *rec = p.records + (ck0 * p.H + h) * kDeltaRecordBytes;
+    if (lead && nck > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    Ring<kDeep> r;
+    int n = 0;
+    // Turn c: the bound of chunk c, then T of chunk c + 2 over that of chunk c, once M has taken it
+    for (int c = -2; c < nck; ++c) {
+      if (c >= 0) {
+        bool ok = wait(BAR_VG + r.at, r.parity);
+        ok = wait(BAR_TILE + r.at, r.parity) && ok;
+        const unsigned char *stage = smem + OFF_VG + r.at * kVG;
+        const int rows = min(C, len - c * C);
+        uint32_t top = 0;
 #pragma unroll 4
-      for (int r = lane >> 3; r < rows; r += 4) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(stage + OFF_V + r * 128 + (lane & 7) * 16);
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
-                                     __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+        for (int i = lane >> 3; i < rows; i += 4) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(stage + i * 128 + (lane & 7) * 16);
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                       __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+        }
+        top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+        const float2 b = reinterpret_cast<const float2 *>(stage + OFF_BETA)[lane];
+        const uint32_t bt = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(b.x), fabsf(b.y))));
+        if (lead) {
+          reinterpret_cast<float *>(smem + OFF_MAXV)[r.at] = __uint_as_float(top << 16) * fmaxf(1.f, 0.5f * __uint_as_float(bt));
+          mbar_arrive(BAR(BAR_READY + r.at));
+        }
+        __syncwarp();
+        r.next();
+        if (c + 2 < nck) ok = wait2(BAR_M, c) && ok;
+        if (!__all_sync(0xffffffffu, ok)) break;
       }
-      top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-      const float2 b = reinterpret_cast<const float2 *>(stage + OFF_BETA)[lane];
-      const uint32_t bt = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(b.x), fabsf(b.y))));
-      if (lead) {
-        reinterpret_cast<float *>(smem + OFF_MAXV)[c % kRecStages] = __uint_as_float(top << 16) * fmaxf(1.f, 0.5f * __uint_as_float(bt));
-        mbar_arrive(BAR(BAR_READY + c % kRecStages));
+      if (lead && c + 2 < nck) {
+        const uint32_t t = BAR(BAR_T + (c & 1));
+        mbar_arrive_expect_tx(t, kT);
+        bulk_load(sb + OFF_T + (c & 1) * kT, rec + (long long)(c + 2) * p.H * kDeltaRecordBytes, kT, t);
+        ++n;
       }
       __syncwarp();
     }
-    if (lead) {  // every load must land before the CTA may exit
-      int never_abort = 0;
-      for (int k = max(0, nr - kRecStages); k < nr; ++k)
-        mbar_wait(BAR(BAR_RFULL + k % kRecStages), (k / kRecStages) & 1, &never_abort, p.err);
-      for (int k = max(0, nt - 2); k < nt; ++k) mbar_wait(BAR(BAR_TFULL + (k & 1)), (k >> 1) & 1, &never_abort, p.err);
-    }
+    if (lead)
+      for (int k = max(0, n - 2); k < n; ++k) settle(BAR_T + (k & 1), (k >> 1) & 1);
     __syncwarp();
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ M, its columns times
     // rho_j 2^{cs_C - cs_j}, into its operand
-    for (int c = 0; c < nck; ++c) {
-      const bool ok = wait_buf(BAR_M, c);
+    Ring<kDeep> r;
+    for (int c = 0; c < nck; ++c, r.next()) {
+      const bool ok = wait2(BAR_M, c);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const float4 *f = reinterpret_cast<const float4 *>(smem + rec_at(c) + OFF_END);
+      const float4 *f = reinterpret_cast<const float4 *>(smem + OFF_VG + r.at * kVG + OFF_END);
 #pragma unroll 1
       for (int b = 0; b < 2; ++b) {
         const uint32_t at = tmem + TM_M + 64 * (c & 1) + 32 * b + lane_off;
@@ -417,24 +477,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     float2 hold[16];
     float gamma = 0.f, gamma_end = 0.f, beta = 0.f, rho = 0.f, vmax = 0.f;  // of the chunk
     float back_o = 0.f, rho_y = 0.f;                                         // of the y to come
+    Ring<kDeep> ring;  // of the rows to load next
     const auto load_rows = [&](int c) {
-      const unsigned char *stage = smem + rec_at(c);
+      const unsigned char *stage = smem + OFF_VG + ring.at * kVG;
       const auto arr = [&](uint32_t off) { return reinterpret_cast<const float *>(stage + off); };
-      const bool ok = wait_rec(BAR_READY, c);
-      vmax = reinterpret_cast<const float *>(smem + OFF_MAXV)[c % kRecStages];
+      const bool ok = wait(BAR_READY + ring.at, ring.parity);
+      vmax = reinterpret_cast<const float *>(smem + OFF_MAXV)[ring.at];
       gamma = arr(OFF_GAMMA)[row];
       gamma_end = arr(OFF_GAMMA)[C - 1];
-      rho = reinterpret_cast<const float *>(smem + tile_at(c) + (is_q ? OFF_RHOQ : OFF_RHOK))[row];
+      rho = reinterpret_cast<const float *>(smem + ring.at * kTile + (is_q ? OFF_RHOQ : OFF_RHOK))[row];
       if (!is_q) {
         const bool live = c * C + row < len;  // (the rows after may hold anything)
         beta = live ? arr(OFF_BETA)[row] : 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 u = live ? *reinterpret_cast<const uint4 *>(stage + OFF_V + swz(row, 4 * hf + i)) : make_uint4(0, 0, 0, 0);
+          const uint4 u = live ? *reinterpret_cast<const uint4 *>(stage + swz(row, 4 * hf + i)) : make_uint4(0, 0, 0, 0);
           hold[2 * i] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
           hold[2 * i + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
         }
       }
+      ring.next();
       return ok;
     };
     const auto put_y = [&](int c) {  // Q rows: y of chunk c
@@ -560,7 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 15) {
+  if (tid == 0 && misc[1] != 0) latch_error(p.err, (int)SSD_ERR_TIMEOUT);
+  if (warp == 13) {
     tc_fence_after();
     tmem_dealloc(tmem, TM_COLS);
   }
