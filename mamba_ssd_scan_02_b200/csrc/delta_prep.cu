@@ -28,20 +28,25 @@ namespace {
 using namespace delta;
 
 constexpr int C = kDeltaChunk;
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxHeads = 16;                      // heads of a CTA, at most
 constexpr uint32_t kHalf = 16384;
 constexpr int kWPitch = 72;                        // floats; = 8 mod 32: conflict-free fragment reads
 constexpr int kKPitch = 136;                       // halves of a K or Q row
 constexpr int kAPitch = 72;                        // halves of a row of A~
-constexpr uint32_t OFF_K = 0;                      // [128][136] halves: K rows, Q rows
-constexpr uint32_t OFF_G = OFF_K + 128 * kKPitch * 2;   // [64][72] floats: K K^T, columns >= row
+constexpr int kWarpF = 64 + 64 + 64 + 96;          // floats per warp: -beta rho^2, rel, 2^rel, column factors
+constexpr uint32_t OFF_W = 0;                      // per warp: [64][72] floats
+constexpr uint32_t OFF_K = OFF_W;                  // before the heads: [128][136] halves: K rows, Q rows
+constexpr uint32_t OFF_G = OFF_W + kWarps * 64 * kWPitch * 4;  // [64][72] floats: K K^T, columns >= row
 constexpr uint32_t OFF_A = OFF_G + 64 * kWPitch * 4;    // [64][72] halves: A~
 constexpr uint32_t OFF_RHO = OFF_A + 64 * kAPitch * 2;  // rho_k[64]
-constexpr uint32_t OFF_GATE = OFF_RHO + 256;            // per warp: cs hi[64], lo[64], -beta rho^2 [64]
-constexpr uint32_t OFF_W = OFF_GATE + kWarps * 768;     // per warp: [64][72] floats
-constexpr uint32_t kSmem = OFF_W + kWarps * 64 * kWPitch * 4;
-static_assert(kSmem <= 232448, "shared memory");
+constexpr uint32_t OFF_F = OFF_RHO + 256;               // per warp: kWarpF floats
+constexpr uint32_t OFF_DT = OFF_F + kWarps * kWarpF * 4;   // [16][66] (dt, b) of the CTA's heads
+constexpr uint32_t OFF_AB = OFF_DT + kMaxHeads * 66 * 4;   // [16] (A, dt_bias)
+constexpr uint32_t kSmem = OFF_AB + kMaxHeads * 8;
+static_assert(128 * kKPitch * 2 <= kWarps * 64 * kWPitch * 4, "K and Q lie where the heads' blocks will");
+static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
 
 // ---- tf32 block products of the inverse -----------------------------------------------------------
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
@@ -181,13 +186,25 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], c
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// 2^x for x <= 0, to fp32's precision: the whole part of x as an exponent, the rest by exp2f
-__device__ __forceinline__ float exp2_split(double x) {
-  const double w = rint(x);
-  return ldexpf(exp2f((float)(x - w)), (int)fmax(w, -200.0));
+// Exponents of decays are sums of up to 64 steps, whose differences should keep an absolute precision (a
+// relative one of the decay) however large the sums: fixed point with 32 fractional bits.  A step beyond
+// +-2^12 is taken as that: 2^-4096 is zero.
+__device__ __forceinline__ long long decay_step(float A, float d) {  // A d log2(e)
+  constexpr float kHi = 1.44269504f, kLo = 1.92596299e-8f;           // log2(e) in two parts
+  const float x = A * d, xl = fmaf(A, d, -x);
+  const float s = x * kHi;
+  if (!(fabsf(s) < 4096.f)) return s > 0.f ? 4096ll << 32 : -(4096ll << 32);
+  const float w = rintf(s);
+  const float f = (s - w) + (fmaf(x, kHi, -s) + fmaf(x, kLo, xl * kHi));
+  return ((long long)(int)w << 32) + __float2int_rn(f * 4294967296.f);
 }
+__device__ __forceinline__ float exp2_fixed(long long x) {
+  const int w = min(max((int)(x >> 32), -127), 127);
+  return ex2((float)(uint32_t)x * 0x1p-32f) * __uint_as_float((uint32_t)(w + 127) << 23);
+}
+__device__ __forceinline__ float to_float(long long x) { return fmaf((float)(uint32_t)x, 0x1p-32f, (float)(int)(x >> 32)); }
 
-__global__ void __launch_bounds__(kThreads, 1) ssd_delta_front_kernel(const DeltaPlan p) {
+__global__ void __launch_bounds__(kThreads, 2) ssd_delta_front_kernel(const DeltaPlan p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const long long ck = blockIdx.x;
   const int g = blockIdx.y, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -212,63 +229,118 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_delta_front_kernel(const Delt
   unsigned char *tile = p.tiles + (ck * p.G + g) * kDeltaTileBytes;
   float *s_rho = reinterpret_cast<float *>(smem + OFF_RHO);
 
-  // ---- K and Q: a warp takes 16 of the 128 rows
+  const int h0 = g * p.hpg + blockIdx.z * p.heads_per_cta;  // the first of the CTA's heads
+  const int n_heads = min(p.heads_per_cta, p.hpg - (int)blockIdx.z * p.heads_per_cta);
+  uint32_t *s_dt = reinterpret_cast<uint32_t *>(smem + OFF_DT);
+  float2 *s_ab = reinterpret_cast<float2 *>(smem + OFF_AB);
+
+  // ---- dt and b of all heads: 8 loads of each in flight
   {
-    uint2 raw[16];
+    const int hl = tid & (kMaxHeads - 1), h = h0 + hl;
+    const bool on = hl < n_heads;
+    if (on && tid < kMaxHeads) s_ab[hl] = make_float2(p.A[h], p.dt_bias[h]);
+    uint32_t x[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = 16 * warp + i, t = r & 63;
-      const __nv_bfloat16 *src = r < 64 ? static_cast<const __nv_bfloat16 *>(p.k) + (base + t) * p.ks
-                                        : static_cast<const __nv_bfloat16 *>(p.q) + (base + t) * p.qs;
-      raw[i] = t < rows ? *reinterpret_cast<const uint2 *>(src + g * kDState + 4 * lane) : make_uint2(0, 0);
+    for (int i = 0; i < 8; ++i) {
+      const int t = (tid >> 4) + 8 * i;
+      x[i] = 0;
+      if (on && t < rows)
+        x[i] = static_cast<const unsigned short *>(p.dt)[(base + t) * p.ds + h] |
+               (uint32_t)static_cast<const unsigned short *>(p.b)[(base + t) * p.bs + h] << 16;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = 16 * warp + i;
-      const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&raw[i].x));
-      const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&raw[i].y));
-      const uint32_t top = __reduce_max_sync(
-          0xffffffffu, max(max(__float_as_uint(a.x) & 0x7fffffffu, __float_as_uint(a.y) & 0x7fffffffu),
-                           max(__float_as_uint(b.x) & 0x7fffffffu, __float_as_uint(b.y) & 0x7fffffffu)));
-      const uint32_t e = min(max(top >> 23, 1u), 253u);
+    for (int i = 0; i < 8; ++i) s_dt[hl * 66 + (tid >> 4) + 8 * i] = x[i];
+  }
+  // ---- K and Q: a warp takes 16 of the 128 rows at a time, a half warp a row, a lane 8 elements
+#pragma unroll 1
+  for (int r0 = 16 * warp; r0 < 128; r0 += 16 * kWarps) {
+    uint4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + 2 * i + (lane >> 4), t = r & 63;
+      const __nv_bfloat16 *src = r0 < 64 ? static_cast<const __nv_bfloat16 *>(p.k) + (base + t) * p.ks
+                                         : static_cast<const __nv_bfloat16 *>(p.q) + (base + t) * p.qs;
+      x[i] = t < rows ? *reinterpret_cast<const uint4 *>(src + g * kDState + 8 * (lane & 15)) : make_uint4(0, 0, 0, 0);
+    }
+    uint32_t m[4];  // the largest magnitudes of two rows each
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      constexpr uint32_t kAbs = 0x7fff7fffu;
+      const uint32_t u = __vmaxu2(__vmaxu2(x[i].x & kAbs, x[i].y & kAbs), __vmaxu2(x[i].z & kAbs, x[i].w & kAbs));
+      const uint32_t top = max(u & 0xffffu, u >> 16);
+      m[i / 2] = i & 1 ? m[i / 2] | top << 16 : top;
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m[k] = __vmaxu2(m[k], __shfl_xor_sync(0xffffffffu, m[k], o));
+    float sq[8], e2[8];  // a row's sum of squares (of this lane's elements); the power of two below its largest
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t e = min(max((i & 1 ? m[i / 2] >> 16 : m[i / 2] & 0xffffu) >> 7, 1u), 253u);
       const float f = __uint_as_float((254u - e) << 23);
-      const uint2 v = make_uint2(h2(__floats2half2_rn(a.x * f, a.y * f)), h2(__floats2half2_rn(b.x * f, b.y * f)));
-      *reinterpret_cast<uint2 *>(smem + OFF_K + r * kKPitch * 2 + 8 * lane) = v;
-      if (blockIdx.z == 0)
-        *reinterpret_cast<uint2 *>(tile + (lane >> 4) * kHalf + swz(r, (lane & 15) >> 1) + 8 * (lane & 1)) = v;
-      float rho = __uint_as_float(e << 23);
-      if (p.qk_norm) rho *= 1.f / sqrtf(warp_sum(a.x * a.x + a.y * a.y + b.x * b.x + b.y * b.y) + p.qk_eps);
-      if (r >= 64) rho *= p.q_scale;
-      if (lane == 0) {
-        if (blockIdx.z == 0) reinterpret_cast<float *>(tile + 2 * kHalf)[r] = rho;
-        if (r < 64) s_rho[r] = rho;
+      e2[i] = __uint_as_float(e << 23);
+      const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t v[4];
+      sq[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = __uint_as_float(u[k] << 16), b = __uint_as_float(u[k] & 0xffff0000u);
+        sq[i] = fmaf(a, a, fmaf(b, b, sq[i]));
+        v[k] = h2(__floats2half2_rn(a * f, b * f));
       }
+      const int r = r0 + 2 * i + (lane >> 4), c = lane & 15;
+      const uint4 o = make_uint4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<uint4 *>(smem + OFF_K + r * kKPitch * 2 + 16 * c) = o;
+      if (blockIdx.z == 0) *reinterpret_cast<uint4 *>(tile + (c >> 3) * kHalf + swz(r, c & 7)) = o;
+    }
+    // sums over 16 lanes; lane c of a half warp ends with row c / 2's
+#pragma unroll
+    for (int o = 8, n = 4; o > 1; o >>= 1, n >>= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float give = up ? sq[i] : sq[i + n];
+        sq[i] = (up ? sq[i + n] : sq[i]) + __shfl_xor_sync(0xffffffffu, give, o);
+        e2[i] = up ? e2[i + n] : e2[i];
+      }
+    }
+    sq[0] += __shfl_xor_sync(0xffffffffu, sq[0], 1);
+    float rho = e2[0];
+    if (p.qk_norm) rho *= 1.f / sqrtf(sq[0] + p.qk_eps);
+    if (r0 >= 64) rho *= p.q_scale;
+    if ((lane & 1) == 0) {
+      const int r = r0 + (lane & 14) + (lane >> 4);
+      if (blockIdx.z == 0) reinterpret_cast<float *>(tile + 2 * kHalf)[r] = rho;
+      if (r < 64) s_rho[r] = rho;
     }
   }
   __syncthreads();
-  // ---- K K^T (warps 0-3, 16 rows each, columns from the diagonal on) and A~ (warps 4-7, up to it)
-  {
-    const int rt = warp & 3, lo = warp < 4 ? 2 * rt : 0, hi = warp < 4 ? 8 : 2 * rt + 2;
+  // ---- K K^T (its columns from the diagonal on) and A~ (up to it), 16 rows per turn of a warp
+#pragma unroll 1
+  for (int rb = warp; rb < 8; rb += kWarps) {
+    const int rt = rb & 3, lo = rb < 4 ? 2 * rt : 0, hi = rb < 4 ? 8 : 2 * rt + 2;
     const uint32_t kq = tc::smem_u32(smem + OFF_K);
-    const uint32_t arow = kq + (16 * warp + (lane & 15)) * kKPitch * 2 + (lane >> 4) * 16;
-    const uint32_t brow = kq + (lane & 7) * kKPitch * 2 + (lane >> 3 & 1) * 16;
+    const uint32_t arow = kq + (16 * rb + (lane & 15)) * kKPitch * 2 + (lane >> 4) * 16;
+    const uint32_t brow = kq + (lane & 7) * kKPitch * 2 + (lane >> 3) * 16;
     uint32_t a[8][4];
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) ldmatrix4(a[ks], arow + 32 * ks);
+#pragma unroll 1
     for (int nt = lo; nt < hi; ++nt) {
       float c0[4] = {}, c1[4] = {};
 #pragma unroll
       for (int ks = 0; ks < 8; ks += 2) {
-        uint32_t b[2], d[2];
-        ldmatrix2(b, brow + 8 * nt * kKPitch * 2 + 32 * ks);
-        ldmatrix2(d, brow + 8 * nt * kKPitch * 2 + 32 * ks + 32);
-        mma_f16(c0, a[ks], b);
-        mma_f16(c1, a[ks + 1], d);
+        uint32_t b[4];
+        ldmatrix4(b, brow + 8 * nt * kKPitch * 2 + 32 * ks);
+        const uint32_t b0[2] = {b[0], b[1]}, b1[2] = {b[2], b[3]};
+        mma_f16(c0, a[ks], b0);
+        mma_f16(c1, a[ks + 1], b1);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) c0[e] += c1[e];
       const int r = 16 * rt + (lane >> 2), j = 8 * nt + 2 * (lane & 3);
-      if (warp < 4) {
+      if (rb < 4) {
         float *o = reinterpret_cast<float *>(smem + OFF_G) + r * kWPitch + j;
         *reinterpret_cast<float2 *>(o) = make_float2(c0[0], c0[1]);
         *reinterpret_cast<float2 *>(o + 8 * kWPitch) = make_float2(c0[2], c0[3]);
@@ -283,54 +355,56 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_delta_front_kernel(const Delt
 
   // ---- heads
   float *w = reinterpret_cast<float *>(smem + OFF_W) + warp * 64 * kWPitch;
-  float *s_hi = reinterpret_cast<float *>(smem + OFF_GATE) + warp * 192, *s_lo = s_hi + 64, *s_f = s_hi + 128;
+  float *s_f = reinterpret_cast<float *>(smem + OFF_F) + warp * kWarpF, *s_rel = s_f + 64, *s_row = s_f + 128, *s_col = s_f + 192;
   const float *gm = reinterpret_cast<const float *>(smem + OFF_G);
-  const int h_end = min((blockIdx.z + 1) * p.heads_per_cta, p.hpg);
-  for (int hh = blockIdx.z * p.heads_per_cta + warp; hh < h_end; hh += kWarps) {
-    const int h = g * p.hpg + hh;
-    unsigned char *rec = p.records + (ck * p.H + h) * kDeltaRecordBytes;
+  for (int hh = warp; hh < n_heads; hh += kWarps) {
+    unsigned char *rec = p.records + (ck * p.H + h0 + hh) * kDeltaRecordBytes;
     {  // gates of tokens 2 lane, 2 lane + 1
-      const float A = p.A[h], bias = p.dt_bias[h];
-      double s[2];
+      const float2 ab = s_ab[hh];
+      const uint2 raw = *reinterpret_cast<const uint2 *>(s_dt + 66 * hh + 2 * lane);
+      const float2 rho = *reinterpret_cast<const float2 *>(s_rho + 2 * lane);
+      long long s[2];
       float beta[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int t = 2 * lane + u;
-        s[u] = 0.0;
-        beta[u] = 0.f;
-        if (t < rows) {
-          float d = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.dt)[(base + t) * p.ds + h]) + bias;
-          const float b = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.b)[(base + t) * p.bs + h]);
-          if (p.softplus) d = d > 20.f ? d : log1pf(expf(d));
-          d = fminf(fmaxf(d, p.dt_min), p.dt_max);
-          s[u] = (double)A * d * 1.4426950408889634;
-          beta[u] = p.beta_scale * (p.beta_sigmoid ? 1.f / (1.f + expf(-b)) : b);
-        }
+        const uint32_t x = u ? raw.y : raw.x;
+        float d = __uint_as_float(x << 16) + ab.y;
+        const float b = __uint_as_float(x & 0xffff0000u);
+        if (p.softplus) d = d > 20.f ? d : log1pf(expf(d));
+        d = d < p.dt_min ? p.dt_min : d > p.dt_max ? p.dt_max : d;
+        const bool on = 2 * lane + u < rows;
+        s[u] = on ? decay_step(ab.x, d) : 0;
+        beta[u] = on ? p.beta_scale * (p.beta_sigmoid ? 1.f / (1.f + expf(-b)) : b) : 0.f;
+        if (on && isnan(ab.x * d)) beta[u] = __int_as_float(0x7fffffff);  // not lost in the fixed point
       }
       s[1] += s[0];
-      double sum = s[1];
+      long long sum = s[1];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, sum, o);
+        const long long x = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += x;
       }
-      const double cs[2] = {sum - s[1] + s[0], sum};
-      const double end = __shfl_sync(0xffffffffu, sum, 31);
-      float gamma[2], to_end[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float rho = s_rho[2 * lane + u];
-        gamma[u] = exp2_split(cs[u]);
-        to_end[u] = rho * exp2_split(end - cs[u]);
-        const float hi = (float)cs[u];
-        s_hi[2 * lane + u] = hi;
-        s_lo[2 * lane + u] = (float)(cs[u] - hi);
-        s_f[2 * lane + u] = -beta[u] * rho * rho;
-      }
+      const long long cs0 = sum - s[1] + s[0], cs1 = sum;
+      const long long end = __shfl_sync(0xffffffffu, sum, 31);
       float2 *o = reinterpret_cast<float2 *>(rec + 3 * 8192) + lane;
       o[0] = make_float2(beta[0], beta[1]);
-      o[32] = make_float2(gamma[0], gamma[1]);
-      o[64] = make_float2(to_end[0], to_end[1]);
+      o[32] = make_float2(exp2_fixed(cs0), exp2_fixed(cs1));
+      o[64] = make_float2(rho.x * exp2_fixed(end - cs0), rho.y * exp2_fixed(end - cs1));
+      *reinterpret_cast<float2 *>(s_f + 2 * lane) = make_float2(-beta[0] * rho.x * rho.x, -beta[1] * rho.y * rho.y);
+      // for A T: cs relative to the first token of its 16; rho 2^(that - cs) for the tokens before
+      long long ref[4];
+#pragma unroll
+      for (int tb = 1; tb < 4; ++tb) {
+        ref[tb] = __shfl_sync(0xffffffffu, cs0, 8 * tb);
+        if (lane < 8 * tb)
+          *reinterpret_cast<float2 *>(s_col + 8 * tb * (tb - 1) + 2 * lane) =
+              make_float2(rho.x * exp2_fixed(ref[tb] - cs0), rho.y * exp2_fixed(ref[tb] - cs1));
+      }
+      ref[0] = __shfl_sync(0xffffffffu, cs0, 0);
+      const long long mine = lane < 16 ? (lane < 8 ? ref[0] : ref[1]) : (lane < 24 ? ref[2] : ref[3]);
+      const float r0 = to_float(cs0 - mine), r1 = to_float(cs1 - mine);
+      *reinterpret_cast<float2 *>(s_rel + 2 * lane) = make_float2(r0, r1);
+      *reinterpret_cast<float2 *>(s_row + 2 * lane) = make_float2(ex2(r0), ex2(r1));
     }
     __syncwarp();
     // w = (-L~)^T by 16 x 16 blocks on and above the diagonal
@@ -374,26 +448,38 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_delta_front_kernel(const Delt
       put_block<4>(w + 16 * kWPitch + 32, d1, lane);
     }
     __syncwarp();
-    // T operands: 8 elements of a row per lane; hi also over the row in w, for A T
+    // T operands: 8 elements of a row per lane, of the blocks on and above the diagonal; hi also over the
+    // row in w, for A T (a unit's place there was read by its own or an earlier lane)
     __half *th = reinterpret_cast<__half *>(w);
-#pragma unroll 4
-    for (int it = 0; it < 16; ++it) {
-      const int j = 4 * it + (lane >> 3), u = lane & 7;
-      const float *src = w + j * kWPitch + 8 * u;
-      const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
-      uint4 hv, lv;
-      split2(make_float2(a.x, a.y), hv.x, lv.x);
-      split2(make_float2(a.z, a.w), hv.y, lv.y);
-      split2(make_float2(b.x, b.y), hv.z, lv.z);
-      split2(make_float2(b.z, b.w), hv.w, lv.w);
-      if ((u >> 1) < (j >> 4)) hv = lv = make_uint4(0, 0, 0, 0);  // below the diagonal blocks: not computed
-      __syncwarp();
-      *reinterpret_cast<uint4 *>(th + j * 2 * kWPitch + 8 * u) = hv;
-      *reinterpret_cast<uint4 *>(rec + swz(j, u)) = hv;
-      *reinterpret_cast<uint4 *>(rec + 8192 + swz(j, u)) = lv;
+#pragma unroll
+    for (int rb = 0; rb < 4; ++rb) {
+      constexpr uint4 zero = {0, 0, 0, 0};
+      const int units = 8 - 2 * rb;
+#pragma unroll 1
+      for (int x = lane; x < 16 * units; x += 32) {
+        const int j = 16 * rb + x / units, u = 2 * rb + x % units;
+        const float *src = w + j * kWPitch + 8 * u;
+        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
+        uint4 hv, lv;
+        split2(make_float2(a.x, a.y), hv.x, lv.x);
+        split2(make_float2(a.z, a.w), hv.y, lv.y);
+        split2(make_float2(b.x, b.y), hv.z, lv.z);
+        split2(make_float2(b.z, b.w), hv.w, lv.w);
+        __syncwarp();
+        *reinterpret_cast<uint4 *>(th + j * 2 * kWPitch + 8 * u) = hv;
+        *reinterpret_cast<uint4 *>(rec + swz(j, u)) = hv;
+        *reinterpret_cast<uint4 *>(rec + 8192 + swz(j, u)) = lv;
+      }
+#pragma unroll
+      for (int x = lane; x < 32 * rb; x += 32) {
+        const int j = 16 * rb + (x & 15), u = x >> 4;
+        *reinterpret_cast<uint4 *>(rec + swz(j, u)) = zero;
+        *reinterpret_cast<uint4 *>(rec + 8192 + swz(j, u)) = zero;
+      }
     }
     __syncwarp();
-    // A T: tiles on and below the diagonal
+    // A T: tiles on and below the diagonal.  Decays to a token of an earlier 16 in two factors, both at most
+    // one: from the first token of t's 16 on, and up to it.
     const uint32_t aa = tc::smem_u32(smem + OFF_A) + (lane & 15) * kAPitch * 2 + (lane >> 4) * 16;
     const uint32_t tt = tc::smem_u32(th) + (lane & 7) * 4 * kWPitch + (lane >> 3 & 1) * 16;
     unsigned char *out = rec + 2 * 8192 + 4 * (lane & 3);
@@ -403,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_delta_front_kernel(const Delt
 #pragma unroll
       for (int kk = 0; kk <= mt; ++kk) ldmatrix4(a[kk], aa + 16 * mt * kAPitch * 2 + 32 * kk);
       const int t = 16 * mt + (lane >> 2);
-      const float hi0 = s_hi[t], lo0 = s_lo[t], hi1 = s_hi[t + 8], lo1 = s_lo[t + 8];
+      const float rt0 = s_row[t], rt1 = s_row[t + 8];
 #pragma unroll
       for (int nt = 0; nt < 2 * mt + 2; ++nt) {
         float c[4] = {};
@@ -414,13 +500,21 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_delta_front_kernel(const Delt
           mma_f16(c, a[kk], b);
         }
         const int j = 8 * nt + 2 * (lane & 3);
-        const float2 hj = *reinterpret_cast<const float2 *>(s_hi + j), lj = *reinterpret_cast<const float2 *>(s_lo + j);
-        const float2 rj = *reinterpret_cast<const float2 *>(s_rho + j);
-        // (above the diagonal the products are zero; the exponent is kept from overflowing there)
-        c[0] *= rj.x * ex2(fminf((hi0 - hj.x) + (lo0 - lj.x), 0.f));
-        c[1] *= rj.y * ex2(fminf((hi0 - hj.y) + (lo0 - lj.y), 0.f));
-        c[2] *= rj.x * ex2(fminf((hi1 - hj.x) + (lo1 - lj.x), 0.f));
-        c[3] *= rj.y * ex2(fminf((hi1 - hj.y) + (lo1 - lj.y), 0.f));
+        if (nt < 2 * mt) {
+          const float2 f = *reinterpret_cast<const float2 *>(s_col + 8 * mt * (mt - 1) + j);
+          c[0] *= rt0 * f.x;
+          c[1] *= rt0 * f.y;
+          c[2] *= rt1 * f.x;
+          c[3] *= rt1 * f.y;
+        } else {
+          const float d0 = s_rel[t], d1 = s_rel[t + 8];
+          const float2 d = *reinterpret_cast<const float2 *>(s_rel + j), r = *reinterpret_cast<const float2 *>(s_rho + j);
+          // (above the diagonal the products are zero, and the decays could overflow)
+          c[0] *= r.x * ex2(j <= t ? d0 - d.x : 0.f);
+          c[1] *= r.y * ex2(j + 1 <= t ? d0 - d.y : 0.f);
+          c[2] *= r.x * ex2(j <= t + 8 ? d1 - d.x : 0.f);
+          c[3] *= r.y * ex2(j + 1 <= t + 8 ? d1 - d.y : 0.f);
+        }
         *reinterpret_cast<uint32_t *>(out + swz(t, nt)) = h2(__floats2half2_rn(c[0], c[1]));
         *reinterpret_cast<uint32_t *>(out + swz(t + 8, nt)) = h2(__floats2half2_rn(c[2], c[3]));
       }
@@ -442,7 +536,7 @@ cudaError_t launch_delta_front(const DeltaPlan &p_in, cudaStream_t s) {
   // As many heads per CTA as share its K K^T, but CTAs for every SM: one head per warp where the chunks
   // and groups alone are few.
   DeltaPlan p = p_in;
-  p.heads_per_cta = p.n_chunks * p.G >= 2 * 148 ? 2 * kWarps : kWarps;
+  p.heads_per_cta = p.n_chunks * p.G >= 2 * 148 ? kMaxHeads : kWarps;
   const dim3 grid((unsigned)p.n_chunks, p.G, (p.hpg + p.heads_per_cta - 1) / p.heads_per_cta);
   ssd_delta_front_kernel<<<grid, kThreads, kSmem, s>>>(p);
   return cudaGetLastError();
