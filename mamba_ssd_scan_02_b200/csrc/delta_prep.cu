@@ -32,21 +32,33 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxHeads = 16;                      // heads of a CTA, at most
 constexpr uint32_t kHalf = 16384;
-constexpr int kWPitch = 72;                        // floats; = 8 mod 32: conflict-free fragment reads
 constexpr int kKPitch = 136;                       // halves of a K or Q row
-constexpr int kAPitch = 72;                        // halves of a row of A~
-constexpr int kWarpF = 64 + 64 + 64 + 96;          // floats per warp: -beta rho^2, rel, 2^rel, column factors
-constexpr uint32_t OFF_W = 0;                      // per warp: [64][72] floats
+constexpr int kWarpF = 64 + 64 + 96;               // floats per warp: -beta rho^2, rel, column factors
+// An upper triangular 64 x 64 of floats, by blocks of 16 rows, each from its diagonal block on: row j's column
+// i (i >= 16 (j / 16)) at row_at(j) + i.  The pitches are 8 mod 16: conflict-free reads of 4 x 8 fragments,
+// and 12 KB instead of 18 (three CTAs per SM instead of two).
+__host__ __device__ constexpr int pitch(int j) { return 72 - 16 * (j >> 4); }
+__host__ __device__ constexpr int row_start(int j) {
+  return 1152 * (j >> 4) - 128 * (j >> 4) * ((j >> 4) - 1) + (j & 15) * pitch(j);
+}
+__host__ __device__ constexpr int row_at(int j) { return row_start(j) - 16 * (j >> 4); }
+constexpr int kTri = row_start(63) + 24;
+// A lower triangular one of halves (A~): rows of block b hold columns 0 .. 16 b + 15
+__host__ __device__ constexpr int a_pitch(int t) { return 24 + 16 * (t >> 4); }
+__host__ __device__ constexpr int a_row(int t) {
+  return 384 * (t >> 4) + 128 * (t >> 4) * ((t >> 4) - 1) + (t & 15) * a_pitch(t);
+}
+constexpr uint32_t OFF_W = 0;                      // per warp: (-L~)^T, then T~^T
 constexpr uint32_t OFF_K = OFF_W;                  // before the heads: [128][136] halves: K rows, Q rows
-constexpr uint32_t OFF_G = OFF_W + kWarps * 64 * kWPitch * 4;  // [64][72] floats: K K^T, columns >= row
-constexpr uint32_t OFF_A = OFF_G + 64 * kWPitch * 4;    // [64][72] halves: A~
-constexpr uint32_t OFF_RHO = OFF_A + 64 * kAPitch * 2;  // rho_k[64]
+constexpr uint32_t OFF_G = OFF_W + kWarps * kTri * 4;   // K K^T, columns >= row
+constexpr uint32_t OFF_A = OFF_G + kTri * 4;            // A~
+constexpr uint32_t OFF_RHO = OFF_A + (a_row(63) + 72) * 2;  // rho_k[64]
 constexpr uint32_t OFF_F = OFF_RHO + 256;               // per warp: kWarpF floats
 constexpr uint32_t OFF_DT = OFF_F + kWarps * kWarpF * 4;   // [16][66] (dt, b) of the CTA's heads
 constexpr uint32_t OFF_AB = OFF_DT + kMaxHeads * 66 * 4;   // [16] (A, dt_bias)
 constexpr uint32_t kSmem = OFF_AB + kMaxHeads * 8;
-static_assert(128 * kKPitch * 2 <= kWarps * 64 * kWPitch * 4, "K and Q lie where the heads' blocks will");
-static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
+static_assert(128 * kKPitch * 2 <= kWarps * kTri * 4, "K and Q lie where the heads' blocks will");
+static_assert(3 * (kSmem + 1024) <= 233472, "three CTAs per SM");
 
 // ---- tf32 block products of the inverse -----------------------------------------------------------
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
@@ -66,24 +78,24 @@ struct FragA {
 struct FragB {
   uint32_t h[2], l[2];
 };
-// 16 x 8 of A, row-major at a
-__device__ __forceinline__ FragA load_a(const float *a, int lane) {
-  const float *x = a + (lane >> 2) * kWPitch + (lane & 3);
+// rows r .. r + 15 and columns c .. c + 7 of w
+__device__ __forceinline__ FragA load_a(const float *w, int r, int c, int lane) {
+  const float *x = w + row_at(r) + c + (lane >> 2) * pitch(r) + (lane & 3);
   FragA f;
   split_tf32(x[0], f.h[0], f.l[0]);
-  split_tf32(x[8 * kWPitch], f.h[1], f.l[1]);
+  split_tf32(x[8 * pitch(r)], f.h[1], f.l[1]);
   split_tf32(x[4], f.h[2], f.l[2]);
-  split_tf32(x[8 * kWPitch + 4], f.h[3], f.l[3]);
+  split_tf32(x[8 * pitch(r) + 4], f.h[3], f.l[3]);
   return f;
 }
-// 8 x 8 of B, row-major at b: its rows r0 and r1 per lane are t and t + 4, or, where A comes from an
+// rows r .. r + 7 and columns c .. c + 7 of w; a lane's two rows are t and t + 4, or, where A comes from an
 // accumulator (from_acc), 2t and 2t + 1
-__device__ __forceinline__ FragB load_b(const float *b, bool from_acc, int lane) {
+__device__ __forceinline__ FragB load_b(const float *w, int r, int c, bool from_acc, int lane) {
   const int t = lane & 3;
-  const float *x = b + (from_acc ? 2 * t : t) * kWPitch + (lane >> 2);
+  const float *x = w + row_at(r) + c + (from_acc ? 2 * t : t) * pitch(r) + (lane >> 2);
   FragB f;
   split_tf32(x[0], f.h[0], f.l[0]);
-  split_tf32(x[from_acc ? kWPitch : 4 * kWPitch], f.h[1], f.l[1]);
+  split_tf32(x[from_acc ? pitch(r) : 4 * pitch(r)], f.h[1], f.l[1]);
   return f;
 }
 // An accumulator tile as an A fragment: a lane's elements of a row are columns 2t and 2t + 1, which the
@@ -97,14 +109,15 @@ __device__ __forceinline__ FragA acc_as_a(const float (&c)[4]) {
   return f;
 }
 
-// W12 = W11 Z W22, the block that joins two inverted diagonal blocks of 8 K rows (transposed, so upper
-// triangular): rows 16 mt .. of it into d.  w11, z and w22 at their corners.  Straight-line: with a branch
-// per tile the products of one would wait for those of the one before.
-template <int K, int MT>
-__device__ __forceinline__ void join(const float *w11, const float *z, const float *w22, float (&d)[K][4], int lane) {
+// W12 = W11 Z W22, the block that joins two inverted diagonal blocks of 8 K rows at P0 and P0 + 8 K (transposed,
+// so upper triangular): its rows 16 MT .. into d.  Straight-line: with a branch per tile the products of one
+// would wait for those of the one before.
+template <int P0, int K, int MT>
+__device__ __forceinline__ void join(const float *w, float (&d)[K][4], int lane) {
+  constexpr int P1 = P0 + 8 * K;
   FragA a[K];
 #pragma unroll
-  for (int kk = 2 * MT; kk < K; ++kk) a[kk] = load_a(w11 + 16 * MT * kWPitch + 8 * kk, lane);
+  for (int kk = 2 * MT; kk < K; ++kk) a[kk] = load_a(w, P0 + 16 * MT, P0 + 8 * kk, lane);
 #pragma unroll
   for (int nt = 0; nt < K; ++nt)
 #pragma unroll
@@ -114,7 +127,7 @@ __device__ __forceinline__ void join(const float *w11, const float *z, const flo
     float hh[4] = {}, hl[4] = {}, lh[4] = {};
 #pragma unroll
     for (int kk = 2 * MT; kk < K; ++kk) {
-      const FragB b = load_b(z + 8 * kk * kWPitch + 8 * kt, false, lane);
+      const FragB b = load_b(w, P0 + 8 * kk, P1 + 8 * kt, false, lane);
       mma_tf32(hh, a[kk].h, b.h);
       mma_tf32(hl, a[kk].h, b.l);
       mma_tf32(lh, a[kk].l, b.h);
@@ -124,20 +137,21 @@ __device__ __forceinline__ void join(const float *w11, const float *z, const flo
     const FragA x = acc_as_a(hh);
 #pragma unroll
     for (int nt = kt; nt < K; ++nt) {
-      const FragB b = load_b(w22 + 8 * kt * kWPitch + 8 * nt, true, lane);
+      const FragB b = load_b(w, P1 + 8 * kt, P1 + 8 * nt, true, lane);
       mma_tf32(d[nt], x.l, b.h);
       mma_tf32(d[nt], x.h, b.l);
       mma_tf32(d[nt], x.h, b.h);
     }
   }
 }
-template <int K>
-__device__ __forceinline__ void put_block(float *o, const float (&d)[K][4], int lane) {
+template <int P0, int K, int MT>
+__device__ __forceinline__ void put_block(float *w, const float (&d)[K][4], int lane) {
+  constexpr int r = P0 + 16 * MT;
 #pragma unroll
   for (int nt = 0; nt < K; ++nt) {
-    float *x = o + (lane >> 2) * kWPitch + 8 * nt + 2 * (lane & 3);
+    float *x = w + row_at(r) + P0 + 8 * K + 8 * nt + (lane >> 2) * pitch(r) + 2 * (lane & 3);
     *reinterpret_cast<float2 *>(x) = make_float2(d[nt][0], d[nt][1]);
-    *reinterpret_cast<float2 *>(x + 8 * kWPitch) = make_float2(d[nt][2], d[nt][3]);
+    *reinterpret_cast<float2 *>(x + 8 * pitch(r)) = make_float2(d[nt][2], d[nt][3]);
   }
 }
 
@@ -147,7 +161,8 @@ __device__ __forceinline__ void put_block(float *o, const float (&d)[K][4], int 
 // multiply-add per row).  z = (-L~)^T at w; a row is read while the one before is used.
 __device__ __forceinline__ void invert16(const float *w, int p0, int lane, float2 (&t)[8]) {
   const int b0 = p0 + (lane & 16), j = lane & 15;
-  const float *zr = w + b0 * kWPitch + b0;
+  const int step = pitch(b0);
+  const float *zr = w + row_start(b0);
   float4 z[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -163,7 +178,7 @@ __device__ __forceinline__ void invert16(const float *w, int p0, int lane, float
     for (int q = m / 4; q < 4; ++q) {
       if (2 * q >= (m + 1) / 2) t[2 * q] = __ffma2_rn(make_float2(z[q].x, z[q].y), t2, t[2 * q]);
       if (2 * q + 1 >= (m + 1) / 2) t[2 * q + 1] = __ffma2_rn(make_float2(z[q].z, z[q].w), t2, t[2 * q + 1]);
-      if (m < 14 && q >= (m + 1) / 4) z[q] = *reinterpret_cast<const float4 *>(zr + (m + 1) * kWPitch + 4 * q);
+      if (m < 14 && q >= (m + 1) / 4) z[q] = *reinterpret_cast<const float4 *>(zr + (m + 1) * step + 4 * q);
     }
   }
 }
@@ -204,7 +219,7 @@ __device__ __forceinline__ float exp2_fixed(long long x) {
 }
 __device__ __forceinline__ float to_float(long long x) { return fmaf((float)(uint32_t)x, 0x1p-32f, (float)(int)(x >> 32)); }
 
-__global__ void __launch_bounds__(kThreads, 2) ssd_delta_front_kernel(const DeltaPlan p) {
+__global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const DeltaPlan p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const long long ck = blockIdx.x;
   const int g = blockIdx.y, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -234,34 +249,42 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_delta_front_kernel(const Delt
   uint32_t *s_dt = reinterpret_cast<uint32_t *>(smem + OFF_DT);
   float2 *s_ab = reinterpret_cast<float2 *>(smem + OFF_AB);
 
-  // ---- dt and b of all heads: 8 loads of each in flight
-  {
-    const int hl = tid & (kMaxHeads - 1), h = h0 + hl;
-    const bool on = hl < n_heads;
-    if (on && tid < kMaxHeads) s_ab[hl] = make_float2(p.A[h], p.dt_bias[h]);
-    uint32_t x[8];
+  // Rows after the chunk's last are loaded as that one and then taken as zero: a load under a condition
+  // becomes a branch, and the loads would wait for each other.
+  // ---- loads, all in flight: dt and b of the heads; K and Q: a warp takes 16 rows of each, a half warp a row,
+  // a lane 8 elements
+  uint4 kq[2][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int t = (tid >> 4) + 8 * i;
-      x[i] = 0;
-      if (on && t < rows)
-        x[i] = static_cast<const unsigned short *>(p.dt)[(base + t) * p.ds + h] |
-               (uint32_t)static_cast<const unsigned short *>(p.b)[(base + t) * p.bs + h] << 16;
-    }
+  for (int m = 0; m < 2; ++m) {
+    const long long stride = m == 0 ? p.ks : p.qs;
+    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(m == 0 ? p.k : p.q) + base * stride + g * kDState + 8 * (lane & 15);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_dt[hl * 66 + (tid >> 4) + 8 * i] = x[i];
+    for (int i = 0; i < 8; ++i)
+      kq[m][i] = *reinterpret_cast<const uint4 *>(src + min(16 * warp + 2 * i + (lane >> 4), rows - 1) * stride);
   }
-  // ---- K and Q: a warp takes 16 of the 128 rows at a time, a half warp a row, a lane 8 elements
-#pragma unroll 1
-  for (int r0 = 16 * warp; r0 < 128; r0 += 16 * kWarps) {
-    uint4 x[8];
+  {
+    const int hl = tid & (kMaxHeads - 1), h = h0 + min(hl, n_heads - 1);
+    const unsigned short *dt = static_cast<const unsigned short *>(p.dt) + base * p.ds + h;
+    const unsigned short *b = static_cast<const unsigned short *>(p.b) + base * p.bs + h;
+    uint32_t x[8], y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = r0 + 2 * i + (lane >> 4), t = r & 63;
-      const __nv_bfloat16 *src = r0 < 64 ? static_cast<const __nv_bfloat16 *>(p.k) + (base + t) * p.ks
-                                         : static_cast<const __nv_bfloat16 *>(p.q) + (base + t) * p.qs;
-      x[i] = t < rows ? *reinterpret_cast<const uint4 *>(src + g * kDState + 8 * (lane & 15)) : make_uint4(0, 0, 0, 0);
+      const int t = min((tid >> 4) + 8 * i, rows - 1);
+      x[i] = dt[t * p.ds];
+      y[i] = b[t * p.bs];
     }
+    if (tid < kMaxHeads) s_ab[hl] = make_float2(p.A[h], p.dt_bias[h]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_dt[hl * 66 + (tid >> 4) + 8 * i] = x[i] | y[i] << 16;
+  }
+  // ---- K and Q
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind) {
+    const int r0 = 64 * kind + 16 * warp;
+    uint4(&x)[8] = kq[kind];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((r0 & 63) + 2 * i + (lane >> 4) >= rows) x[i] = make_uint4(0, 0, 0, 0);
     uint32_t m[4];  // the largest magnitudes of two rows each
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -308,11 +331,11 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_delta_front_kernel(const Delt
     sq[0] += __shfl_xor_sync(0xffffffffu, sq[0], 1);
     float rho = e2[0];
     if (p.qk_norm) rho *= 1.f / sqrtf(sq[0] + p.qk_eps);
-    if (r0 >= 64) rho *= p.q_scale;
+    if (kind == 1) rho *= p.q_scale;
     if ((lane & 1) == 0) {
       const int r = r0 + (lane & 14) + (lane >> 4);
       if (blockIdx.z == 0) reinterpret_cast<float *>(tile + 2 * kHalf)[r] = rho;
-      if (r < 64) s_rho[r] = rho;
+      if (kind == 0) s_rho[r] = rho;
     }
   }
   __syncthreads();
@@ -326,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_delta_front_kernel(const Delt
     uint32_t a[8][4];
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) ldmatrix4(a[ks], arow + 32 * ks);
-#pragma unroll 1
+#pragma unroll 2
     for (int nt = lo; nt < hi; ++nt) {
       float c0[4] = {}, c1[4] = {};
 #pragma unroll
@@ -341,21 +364,21 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_delta_front_kernel(const Delt
       for (int e = 0; e < 4; ++e) c0[e] += c1[e];
       const int r = 16 * rt + (lane >> 2), j = 8 * nt + 2 * (lane & 3);
       if (rb < 4) {
-        float *o = reinterpret_cast<float *>(smem + OFF_G) + r * kWPitch + j;
+        float *o = reinterpret_cast<float *>(smem + OFF_G) + row_at(r) + j;
         *reinterpret_cast<float2 *>(o) = make_float2(c0[0], c0[1]);
-        *reinterpret_cast<float2 *>(o + 8 * kWPitch) = make_float2(c0[2], c0[3]);
+        *reinterpret_cast<float2 *>(o + 8 * pitch(r)) = make_float2(c0[2], c0[3]);
       } else {
-        __half *o = reinterpret_cast<__half *>(smem + OFF_A) + r * kAPitch + j;
+        __half *o = reinterpret_cast<__half *>(smem + OFF_A) + a_row(r) + j;
         *reinterpret_cast<__half2 *>(o) = __floats2half2_rn(j <= r ? c0[0] : 0.f, j + 1 <= r ? c0[1] : 0.f);
-        *reinterpret_cast<__half2 *>(o + 8 * kAPitch) = __floats2half2_rn(j <= r + 8 ? c0[2] : 0.f, j + 1 <= r + 8 ? c0[3] : 0.f);
+        *reinterpret_cast<__half2 *>(o + 8 * a_pitch(r)) = __floats2half2_rn(j <= r + 8 ? c0[2] : 0.f, j + 1 <= r + 8 ? c0[3] : 0.f);
       }
     }
   }
   __syncthreads();
 
   // ---- heads
-  float *w = reinterpret_cast<float *>(smem + OFF_W) + warp * 64 * kWPitch;
-  float *s_f = reinterpret_cast<float *>(smem + OFF_F) + warp * kWarpF, *s_rel = s_f + 64, *s_row = s_f + 128, *s_col = s_f + 192;
+  float *w = reinterpret_cast<float *>(smem + OFF_W) + warp * kTri;
+  float *s_f = reinterpret_cast<float *>(smem + OFF_F) + warp * kWarpF, *s_rel = s_f + 64, *s_col = s_f + 128;
   const float *gm = reinterpret_cast<const float *>(smem + OFF_G);
   for (int hh = warp; hh < n_heads; hh += kWarps) {
     unsigned char *rec = p.records + (ck * p.H + h0 + hh) * kDeltaRecordBytes;
@@ -402,9 +425,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_delta_front_kernel(const Delt
       }
       ref[0] = __shfl_sync(0xffffffffu, cs0, 0);
       const long long mine = lane < 16 ? (lane < 8 ? ref[0] : ref[1]) : (lane < 24 ? ref[2] : ref[3]);
-      const float r0 = to_float(cs0 - mine), r1 = to_float(cs1 - mine);
-      *reinterpret_cast<float2 *>(s_rel + 2 * lane) = make_float2(r0, r1);
-      *reinterpret_cast<float2 *>(s_row + 2 * lane) = make_float2(ex2(r0), ex2(r1));
+      *reinterpret_cast<float2 *>(s_rel + 2 * lane) = make_float2(to_float(cs0 - mine), to_float(cs1 - mine));
     }
     __syncwarp();
     // w = (-L~)^T by 16 x 16 blocks on and above the diagonal
@@ -415,11 +436,11 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_delta_front_kernel(const Delt
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int j = 16 * rb + 8 * u + (lane >> 2), i = 16 * cb + 4 * (lane & 3);
-          const float4 x = *reinterpret_cast<const float4 *>(gm + j * kWPitch + i);
+          const float4 x = *reinterpret_cast<const float4 *>(gm + row_at(16 * rb) + (j & 15) * pitch(16 * rb) + i);
           const float4 f = *reinterpret_cast<const float4 *>(s_f + i);
           float4 y = make_float4(f.x * x.x, f.y * x.y, f.z * x.z, f.w * x.w);
           if (rb == cb) y = make_float4(i > j ? y.x : 0.f, i + 1 > j ? y.y : 0.f, i + 2 > j ? y.z : 0.f, i + 3 > j ? y.w : 0.f);
-          *reinterpret_cast<float4 *>(w + j * kWPitch + i) = y;
+          *reinterpret_cast<float4 *>(w + row_at(16 * rb) + (j & 15) * pitch(16 * rb) + i) = y;
         }
     __syncwarp();
 #pragma unroll 1
@@ -427,30 +448,32 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_delta_front_kernel(const Delt
       float2 t[8];
       invert16(w, p0, lane, t);
       __syncwarp();
-      float *o = w + (p0 + lane) * kWPitch + p0 + (lane & 16);
+      float *o = w + row_start(p0 + lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<float4 *>(o + 4 * i) = make_float4(t[2 * i].x, t[2 * i].y, t[2 * i + 1].x, t[2 * i + 1].y);
+    }
+    __syncwarp();
+    {
+      float d0[2][4], d1[2][4];
+      join<0, 2, 0>(w, d0, lane);
+      join<32, 2, 0>(w, d1, lane);
       __syncwarp();
-      float d[2][4];
-      float *wp = w + p0 * kWPitch + p0;
-      join<2, 0>(wp, wp + 16, wp + 16 * kWPitch + 16, d, lane);
-      __syncwarp();
-      put_block<2>(wp + 16, d, lane);
+      put_block<0, 2, 0>(w, d0, lane);
+      put_block<32, 2, 0>(w, d1, lane);
     }
     __syncwarp();
     {
       float d0[4][4], d1[4][4];
-      join<4, 0>(w, w + 32, w + 32 * kWPitch + 32, d0, lane);
-      join<4, 1>(w, w + 32, w + 32 * kWPitch + 32, d1, lane);
+      join<0, 4, 0>(w, d0, lane);
+      join<0, 4, 1>(w, d1, lane);
       __syncwarp();
-      put_block<4>(w + 32, d0, lane);
-      put_block<4>(w + 16 * kWPitch + 32, d1, lane);
+      put_block<0, 4, 0>(w, d0, lane);
+      put_block<0, 4, 1>(w, d1, lane);
     }
     __syncwarp();
     // T operands: 8 elements of a row per lane, of the blocks on and above the diagonal; hi also over the
     // row in w, for A T (a unit's place there was read by its own or an earlier lane)
-    __half *th = reinterpret_cast<__half *>(w);
 #pragma unroll
     for (int rb = 0; rb < 4; ++rb) {
       constexpr uint4 zero = {0, 0, 0, 0};
@@ -458,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_delta_front_kernel(const Delt
 #pragma unroll 1
       for (int x = lane; x < 16 * units; x += 32) {
         const int j = 16 * rb + x / units, u = 2 * rb + x % units;
-        const float *src = w + j * kWPitch + 8 * u;
+        float *src = w + row_start(16 * rb) + (x / units) * pitch(16 * rb) + 8 * (x % units);
         const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
         uint4 hv, lv;
         split2(make_float2(a.x, a.y), hv.x, lv.x);
@@ -466,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_delta_front_kernel(const Delt
         split2(make_float2(b.x, b.y), hv.z, lv.z);
         split2(make_float2(b.z, b.w), hv.w, lv.w);
         __syncwarp();
-        *reinterpret_cast<uint4 *>(th + j * 2 * kWPitch + 8 * u) = hv;
+        *reinterpret_cast<uint4 *>(src - 4 * (x % units)) = hv;
         *reinterpret_cast<uint4 *>(rec + swz(j, u)) = hv;
         *reinterpret_cast<uint4 *>(rec + 8192 + swz(j, u)) = lv;
       }
@@ -480,23 +503,22 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_delta_front_kernel(const Delt
     __syncwarp();
     // A T: tiles on and below the diagonal.  Decays to a token of an earlier 16 in two factors, both at most
     // one: from the first token of t's 16 on, and up to it.
-    const uint32_t aa = tc::smem_u32(smem + OFF_A) + (lane & 15) * kAPitch * 2 + (lane >> 4) * 16;
-    const uint32_t tt = tc::smem_u32(th) + (lane & 7) * 4 * kWPitch + (lane >> 3 & 1) * 16;
+    const uint32_t aa = tc::smem_u32(smem + OFF_A) + (lane >> 4) * 16, tt = tc::smem_u32(w) + (lane >> 3 & 1) * 16;
     unsigned char *out = rec + 2 * 8192 + 4 * (lane & 3);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
       uint32_t a[4][4];
 #pragma unroll
-      for (int kk = 0; kk <= mt; ++kk) ldmatrix4(a[kk], aa + 16 * mt * kAPitch * 2 + 32 * kk);
+      for (int kk = 0; kk <= mt; ++kk) ldmatrix4(a[kk], aa + 2 * a_row(16 * mt) + (lane & 15) * 2 * a_pitch(16 * mt) + 32 * kk);
       const int t = 16 * mt + (lane >> 2);
-      const float rt0 = s_row[t], rt1 = s_row[t + 8];
+      const float d0 = s_rel[t], d1 = s_rel[t + 8], rt0 = ex2(d0), rt1 = ex2(d1);
 #pragma unroll
       for (int nt = 0; nt < 2 * mt + 2; ++nt) {
         float c[4] = {};
 #pragma unroll
         for (int kk = nt / 2; kk <= mt; ++kk) {
           uint32_t b[2];
-          ldmatrix2(b, tt + 8 * nt * 4 * kWPitch + 32 * kk);
+          ldmatrix2(b, tt + 4 * row_start(8 * nt) + (lane & 7) * 4 * pitch(8 * nt) + 32 * (kk - nt / 2));
           mma_f16(c, a[kk], b);
         }
         const int j = 8 * nt + 2 * (lane & 3);
@@ -507,7 +529,6 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_delta_front_kernel(const Delt
           c[2] *= rt1 * f.x;
           c[3] *= rt1 * f.y;
         } else {
-          const float d0 = s_rel[t], d1 = s_rel[t + 8];
           const float2 d = *reinterpret_cast<const float2 *>(s_rel + j), r = *reinterpret_cast<const float2 *>(s_rho + j);
           // (above the diagonal the products are zero, and the decays could overflow)
           c[0] *= r.x * ex2(j <= t ? d0 - d.x : 0.f);
