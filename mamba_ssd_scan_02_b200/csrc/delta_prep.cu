@@ -473,23 +473,30 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
     }
     __syncwarp();
     // T operands: 8 elements of a row per lane, of the blocks on and above the diagonal; hi also over the
-    // row in w, for A T (a unit's place there was read by its own or an earlier lane)
+    // row in w, for A T
 #pragma unroll
     for (int rb = 0; rb < 4; ++rb) {
       constexpr uint4 zero = {0, 0, 0, 0};
       const int units = 8 - 2 * rb;
-#pragma unroll 1
-      for (int x = lane; x < 16 * units; x += 32) {
-        const int j = 16 * rb + x / units, u = 2 * rb + x % units;
-        float *src = w + row_start(16 * rb) + (x / units) * pitch(16 * rb) + 8 * (x % units);
-        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
+float *row[4];
+      float4 a[4], b[4];
+#pragma unroll
+      for (int k = 0; k < 4 - rb; ++k) {
+        const int x = 32 * k + lane;
+        row[k] = w + row_start(16 * rb) + (x / units) * pitch(16 * rb) + 4 * (x % units);
+        a[k] = *reinterpret_cast<const float4 *>(row[k] + 4 * (x % units));
+        b[k] = *reinterpret_cast<const float4 *>(row[k] + 4 * (x % units) + 4);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 4 - rb; ++k) {
+        const int x = 32 * k + lane, j = 16 * rb + x / units, u = 2 * rb + x % units;
         uint4 hv, lv;
-        split2(make_float2(a.x, a.y), hv.x, lv.x);
-        split2(make_float2(a.z, a.w), hv.y, lv.y);
-        split2(make_float2(b.x, b.y), hv.z, lv.z);
-        split2(make_float2(b.z, b.w), hv.w, lv.w);
-        __syncwarp();
-        *reinterpret_cast<uint4 *>(src - 4 * (x % units)) = hv;
+        split2(make_float2(a[k].x, a[k].y), hv.x, lv.x);
+        split2(make_float2(a[k].z, a[k].w), hv.y, lv.y);
+        split2(make_float2(b[k].x, b[k].y), hv.z, lv.z);
+        split2(make_float2(b[k].z, b[k].w), hv.w, lv.w);
+        *reinterpret_cast<uint4 *>(row[k]) = hv;
         *reinterpret_cast<uint4 *>(rec + swz(j, u)) = hv;
         *reinterpret_cast<uint4 *>(rec + 8192 + swz(j, u)) = lv;
       }
