@@ -34,21 +34,28 @@ constexpr int kMaxHeads = 16;                      // heads of a CTA, at most
 constexpr uint32_t kHalf = 16384;
 constexpr int kKPitch = 136;                       // halves of a K or Q row
 constexpr int kWarpF = 64 + 64 + 96;               // floats per warp: -beta rho^2, rel, column factors
-// An upper triangular 64 x 64 of floats, by blocks of 16 rows, each from its diagonal block on: row j's column
-// i (i >= 16 (j / 16)) at row_at(j) + i.  The pitches are 8 mod 16: conflict-free reads of 4 x 8 fragments,
-// and 12 KB instead of 18 (three CTAs per SM instead of two).
-__host__ __device__ constexpr int pitch(int j) { return 72 - 16 * (j >> 4); }
+// Upper triangular 64 x 64s of floats, by blocks of 16 rows, each from its diagonal block on: 12 KB instead of
+// 18 (three CTAs per SM instead of two).  Row j's column i (i >= 16 (j / 16)) is at row_at(j) + i of T~^T, at
+// g_at(j) + i of K K^T.  The pitches of K K^T are 8 or 24 mod 32 (conflict-free reads of 4 rows x 8), those of
+// T~^T 12 or 20 (of 8 rows x 4, of 4 rows in steps of 2 x 8, and of 8 rows x 16 bytes).
+__host__ __device__ constexpr int pitch(int j) { return j < 32 ? (j < 16 ? 76 : 52) : (j < 48 ? 44 : 20); }
 __host__ __device__ constexpr int row_start(int j) {
-  return 1152 * (j >> 4) - 128 * (j >> 4) * ((j >> 4) - 1) + (j & 15) * pitch(j);
+  return (j < 32 ? (j < 16 ? 0 : 1216) : (j < 48 ? 2048 : 2752)) + (j & 15) * pitch(j);
 }
 __host__ __device__ constexpr int row_at(int j) { return row_start(j) - 16 * (j >> 4); }
-constexpr int kTri = row_start(63) + 24;
+__host__ __device__ constexpr int g_pitch(int j) { return 72 - 16 * (j >> 4); }
+__host__ __device__ constexpr int g_start(int j) {
+  return 1152 * (j >> 4) - 128 * (j >> 4) * ((j >> 4) - 1) + (j & 15) * g_pitch(j);
+}
+__host__ __device__ constexpr int g_at(int j) { return g_start(j) - 16 * (j >> 4); }
+constexpr int kTri = row_start(63) + 20;
+static_assert(g_start(63) + 24 == kTri, "the two layouts have one size");
 // A lower triangular one of halves (A~): rows of block b hold columns 0 .. 16 b + 15
 __host__ __device__ constexpr int a_pitch(int t) { return 24 + 16 * (t >> 4); }
 __host__ __device__ constexpr int a_row(int t) {
   return 384 * (t >> 4) + 128 * (t >> 4) * ((t >> 4) - 1) + (t & 15) * a_pitch(t);
 }
-constexpr uint32_t OFF_W = 0;                      // per warp: (-L~)^T, then T~^T
+constexpr uint32_t OFF_W = 0;                      // per warp: T~^T
 constexpr uint32_t OFF_K = OFF_W;                  // before the heads: [128][136] halves: K rows, Q rows
 constexpr uint32_t OFF_G = OFF_W + kWarps * kTri * 4;   // K K^T, columns >= row
 constexpr uint32_t OFF_A = OFF_G + kTri * 4;            // A~
@@ -88,15 +95,21 @@ __device__ __forceinline__ FragA load_a(const float *w, int r, int c, int lane) 
   split_tf32(x[8 * pitch(r) + 4], f.h[3], f.l[3]);
   return f;
 }
-// rows r .. r + 7 and columns c .. c + 7 of w; a lane's two rows are t and t + 4, or, where A comes from an
-// accumulator (from_acc), 2t and 2t + 1
-__device__ __forceinline__ FragB load_b(const float *w, int r, int c, bool from_acc, int lane) {
-  const int t = lane & 3;
-  const float *x = w + row_at(r) + c + (from_acc ? 2 * t : t) * pitch(r) + (lane >> 2);
+// rows r .. r + 7 and columns c .. c + 7 of w, for an A from an accumulator: a lane's two rows are 2t, 2t + 1
+__device__ __forceinline__ FragB load_b(const float *w, int r, int c, int lane) {
+  const float *x = w + row_at(r) + c + 2 * (lane & 3) * pitch(r) + (lane >> 2);
   FragB f;
   split_tf32(x[0], f.h[0], f.l[0]);
-  split_tf32(x[from_acc ? pitch(r) : 4 * pitch(r)], f.h[1], f.l[1]);
+  split_tf32(x[pitch(r)], f.h[1], f.l[1]);
   return f;
+}
+// rows r .. r + 7 and columns c .. c + 7 of -L~^T, which is K K^T times f = -beta rho^2 of the column
+__device__ __forceinline__ FragB load_z(const float *gm, int r, int c, float f, int lane) {
+  const float *x = gm + g_at(r) + c + (lane & 3) * g_pitch(r) + (lane >> 2);
+  FragB b;
+  split_tf32(f * x[0], b.h[0], b.l[0]);
+  split_tf32(f * x[4 * g_pitch(r)], b.h[1], b.l[1]);
+  return b;
 }
 // An accumulator tile as an A fragment: a lane's elements of a row are columns 2t and 2t + 1, which the
 // product takes as k = t and t + 4 (B's rows permuted alike).
@@ -109,11 +122,11 @@ __device__ __forceinline__ FragA acc_as_a(const float (&c)[4]) {
   return f;
 }
 
-// W12 = W11 Z W22, the block that joins two inverted diagonal blocks of 8 K rows at P0 and P0 + 8 K (transposed,
+// W12 = W11 Z W22 (Z of -L~^T), the block that joins two inverted diagonal blocks of 8 K rows at P0 and P0 + 8 K (transposed,
 // so upper triangular): its rows 16 MT .. into d.  Straight-line: with a branch per tile the products of one
 // would wait for those of the one before.
 template <int P0, int K, int MT>
-__device__ __forceinline__ void join(const float *w, float (&d)[K][4], int lane) {
+__device__ __forceinline__ void join(const float *w, const float *gm, const float *s_f, float (&d)[K][4], int lane) {
   constexpr int P1 = P0 + 8 * K;
   FragA a[K];
 #pragma unroll
@@ -125,9 +138,10 @@ __device__ __forceinline__ void join(const float *w, float (&d)[K][4], int lane)
 #pragma unroll
   for (int kt = 0; kt < K; ++kt) {
     float hh[4] = {}, hl[4] = {}, lh[4] = {};
+    const float f = s_f[P1 + 8 * kt + (lane >> 2)];
 #pragma unroll
     for (int kk = 2 * MT; kk < K; ++kk) {
-      const FragB b = load_b(w, P0 + 8 * kk, P1 + 8 * kt, false, lane);
+      const FragB b = load_z(gm, P0 + 8 * kk, P1 + 8 * kt, f, lane);
       mma_tf32(hh, a[kk].h, b.h);
       mma_tf32(hl, a[kk].h, b.l);
       mma_tf32(lh, a[kk].l, b.h);
@@ -137,7 +151,7 @@ __device__ __forceinline__ void join(const float *w, float (&d)[K][4], int lane)
     const FragA x = acc_as_a(hh);
 #pragma unroll
     for (int nt = kt; nt < K; ++nt) {
-      const FragB b = load_b(w, P1 + 8 * kt, P1 + 8 * nt, true, lane);
+      const FragB b = load_b(w, P1 + 8 * kt, P1 + 8 * nt, lane);
       mma_tf32(d[nt], x.l, b.h);
       mma_tf32(d[nt], x.h, b.l);
       mma_tf32(d[nt], x.h, b.h);
@@ -156,42 +170,40 @@ __device__ __forceinline__ void put_block(float *w, const float (&d)[K][4], int 
 }
 
 // The 16 x 16 diagonal blocks at p0 and p0 + 16, by one warp: t = column `lane & 15` of T~'s block lane / 16,
-//   t_i = [i == j] - sum_{m < i} L~_im t_m,
-// the column of m taken off every later element as soon as t_m is known (so the chain is one
-// multiply-add per row).  z = (-L~)^T at w; a row is read while the one before is used.
-__device__ __forceinline__ void invert16(const float *w, int p0, int lane, float2 (&t)[8]) {
-  const int b0 = p0 + (lane & 16), j = lane & 15;
-  const int step = pitch(b0);
-  const float *zr = w + row_start(b0);
-  float4 z[4];
+//   t_i = [i == j] + f_i sum_{m < i} K_m.K_i t_m,   f = -beta rho^2,
+// the column of m added to every later sum as soon as t_m is known (so the chain is two multiply-adds per
+// row).  A row of K K^T is read while the one before is used.
+__device__ __forceinline__ void invert16(const float *gm, const float *s_f, int p0, int lane, float2 (&t)[8]) {
+  const int b0 = p0 + (lane & 16), j = lane & 15, step = g_pitch(b0);
+  const float *zr = gm + g_start(b0);
+  float4 z[4], f[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     z[q] = *reinterpret_cast<const float4 *>(zr + 4 * q);
-    t[2 * q] = make_float2(4 * q == j ? 1.f : 0.f, 4 * q + 1 == j ? 1.f : 0.f);
-    t[2 * q + 1] = make_float2(4 * q + 2 == j ? 1.f : 0.f, 4 * q + 3 == j ? 1.f : 0.f);
+    f[q] = *reinterpret_cast<const float4 *>(s_f + b0 + 4 * q);
+    t[2 * q] = t[2 * q + 1] = make_float2(0.f, 0.f);
   }
 #pragma unroll
-  for (int m = 0; m < 15; ++m) {
-    const float tm = m & 1 ? t[m / 2].y : t[m / 2].x;
-    const float2 t2 = make_float2(tm, tm);
+  for (int m = 0; m < 16; ++m) {
+    const float fm = m & 2 ? (m & 1 ? f[m / 4].w : f[m / 4].z) : (m & 1 ? f[m / 4].y : f[m / 4].x);
+    float &own = m & 1 ? t[m / 2].y : t[m / 2].x;
+    own = fmaf(fm, own, m == j ? 1.f : 0.f);
+    const float2 t2 = make_float2(own, own);
+    if (!(m & 1)) t[m / 2].y = fmaf(m & 2 ? z[m / 4].w : z[m / 4].y, own, t[m / 2].y);
 #pragma unroll
-    for (int q = m / 4; q < 4; ++q) {
-      if (2 * q >= (m + 1) / 2) t[2 * q] = __ffma2_rn(make_float2(z[q].x, z[q].y), t2, t[2 * q]);
-      if (2 * q + 1 >= (m + 1) / 2) t[2 * q + 1] = __ffma2_rn(make_float2(z[q].z, z[q].w), t2, t[2 * q + 1]);
-      if (m < 14 && q >= (m + 1) / 4) z[q] = *reinterpret_cast<const float4 *>(zr + (m + 1) * step + 4 * q);
+    for (int q = (m + 1) / 4; q < 4; ++q) {
+      if (4 * q > m) t[2 * q] = __ffma2_rn(make_float2(z[q].x, z[q].y), t2, t[2 * q]);
+      if (4 * q + 2 > m) t[2 * q + 1] = __ffma2_rn(make_float2(z[q].z, z[q].w), t2, t[2 * q + 1]);
+      if (m < 14) z[q] = *reinterpret_cast<const float4 *>(zr + (m + 1) * step + 4 * q);
     }
   }
 }
-
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
-}
-__device__ __forceinline__ void ldmatrix2(uint32_t (&r)[2], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm volatile(
@@ -364,9 +376,9 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
       for (int e = 0; e < 4; ++e) c0[e] += c1[e];
       const int r = 16 * rt + (lane >> 2), j = 8 * nt + 2 * (lane & 3);
       if (rb < 4) {
-        float *o = reinterpret_cast<float *>(smem + OFF_G) + row_at(r) + j;
+        float *o = reinterpret_cast<float *>(smem + OFF_G) + g_at(r) + j;
         *reinterpret_cast<float2 *>(o) = make_float2(c0[0], c0[1]);
-        *reinterpret_cast<float2 *>(o + 8 * pitch(r)) = make_float2(c0[2], c0[3]);
+        *reinterpret_cast<float2 *>(o + 8 * g_pitch(r)) = make_float2(c0[2], c0[3]);
       } else {
         __half *o = reinterpret_cast<__half *>(smem + OFF_A) + a_row(r) + j;
         *reinterpret_cast<__half2 *>(o) = __floats2half2_rn(j <= r ? c0[0] : 0.f, j + 1 <= r ? c0[1] : 0.f);
@@ -428,26 +440,10 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
       *reinterpret_cast<float2 *>(s_rel + 2 * lane) = make_float2(to_float(cs0 - mine), to_float(cs1 - mine));
     }
     __syncwarp();
-    // w = (-L~)^T by 16 x 16 blocks on and above the diagonal
-#pragma unroll
-    for (int rb = 0; rb < 4; ++rb)
-#pragma unroll
-      for (int cb = rb; cb < 4; ++cb)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int j = 16 * rb + 8 * u + (lane >> 2), i = 16 * cb + 4 * (lane & 3);
-          const float4 x = *reinterpret_cast<const float4 *>(gm + row_at(16 * rb) + (j & 15) * pitch(16 * rb) + i);
-          const float4 f = *reinterpret_cast<const float4 *>(s_f + i);
-          float4 y = make_float4(f.x * x.x, f.y * x.y, f.z * x.z, f.w * x.w);
-          if (rb == cb) y = make_float4(i > j ? y.x : 0.f, i + 1 > j ? y.y : 0.f, i + 2 > j ? y.z : 0.f, i + 3 > j ? y.w : 0.f);
-          *reinterpret_cast<float4 *>(w + row_at(16 * rb) + (j & 15) * pitch(16 * rb) + i) = y;
-        }
-    __syncwarp();
 #pragma unroll 1
     for (int p0 = 0; p0 < 64; p0 += 32) {
       float2 t[8];
-      invert16(w, p0, lane, t);
-      __syncwarp();
+      invert16(gm, s_f, p0, lane, t);
       float *o = w + row_start(p0 + lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -456,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
     __syncwarp();
     {
       float d0[2][4], d1[2][4];
-      join<0, 2, 0>(w, d0, lane);
-      join<32, 2, 0>(w, d1, lane);
+      join<0, 2, 0>(w, gm, s_f, d0, lane);
+      join<32, 2, 0>(w, gm, s_f, d1, lane);
       __syncwarp();
       put_block<0, 2, 0>(w, d0, lane);
       put_block<32, 2, 0>(w, d1, lane);
@@ -465,8 +461,8 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
     __syncwarp();
     {
       float d0[4][4], d1[4][4];
-      join<0, 4, 0>(w, d0, lane);
-      join<0, 4, 1>(w, d1, lane);
+      join<0, 4, 0>(w, gm, s_f, d0, lane);
+      join<0, 4, 1>(w, gm, s_f, d1, lane);
       __syncwarp();
       put_block<0, 4, 0>(w, d0, lane);
       put_block<0, 4, 1>(w, d1, lane);
@@ -511,6 +507,12 @@ float *row[4];
     // A T: tiles on and below the diagonal.  Decays to a token of an earlier 16 in two factors, both at most
     // one: from the first token of t's 16 on, and up to it.
     const uint32_t aa = tc::smem_u32(smem + OFF_A) + (lane >> 4) * 16, tt = tc::smem_u32(w) + (lane >> 3 & 1) * 16;
+    uint32_t b[4][4][4];  // [16 rows of T~^T][16 columns]: the fragments of two tiles of 8 rows
+#pragma unroll
+    for (int rb = 0; rb < 4; ++rb)
+#pragma unroll
+      for (int kk = rb; kk < 4; ++kk)
+        ldmatrix4(b[rb][kk], tt + 4 * row_start(16 * rb) + ((lane & 7) + (lane >> 4) * 8) * 4 * pitch(16 * rb) + 32 * (kk - rb));
     unsigned char *out = rec + 2 * 8192 + 4 * (lane & 3);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
@@ -524,9 +526,9 @@ float *row[4];
         float c[4] = {};
 #pragma unroll
         for (int kk = nt / 2; kk <= mt; ++kk) {
-          uint32_t b[2];
-          ldmatrix2(b, tt + 4 * row_start(8 * nt) + (lane & 7) * 4 * pitch(8 * nt) + 32 * (kk - nt / 2));
-          mma_f16(c, a[kk], b);
+          const uint32_t(&x)[4] = b[nt / 2][kk];
+          const uint32_t y[2] = {x[2 * (nt & 1)], x[2 * (nt & 1) + 1]};
+          mma_f16(c, a[kk], y);
         }
         const int j = 8 * nt + 2 * (lane & 3);
         if (nt < 2 * mt) {
