@@ -490,7 +490,7 @@ def make_delta_config(cfg: dict, batch: int, seqlen: int, kernel: int | None = N
 
 
 def _check_arg(t, name, dtype, device, shape):
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape:
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be {dtype} {shape} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
@@ -507,11 +507,13 @@ def _rows(t, name, dtype, device, shape):
     evenly spaced: [B, L, width] rows are L * stride apart between batch rows."""
     _check_arg(t, name, dtype, device, shape)
     st = t.stride()
+    if len(shape) == 2 and st[1] == 1:
+        # at most one row: any stride that holds it and keeps the alignment rule
+        return t.data_ptr(), st[0] if shape[0] > 1 else (shape[1] + 7) // 8 * 8
     many = [i for i in range(len(shape) - 1) if shape[i] != 1]
     if st[-1] != 1 and shape[-1] > 1 and 0 not in shape:
         raise ValueError(f"{name}: channels must be contiguous")
     if not many or 0 in shape:
-        # at most one row: any stride that holds it and keeps the alignment rule
         return t.data_ptr(), (shape[-1] + 7) // 8 * 8
     if len(many) == 2 and st[0] != shape[1] * st[1]:
         raise ValueError(f"{name}: batch rows must be seqlen * row_stride apart")
@@ -525,8 +527,8 @@ def _call(fn, where, device, stream, made, *args):
     import torch
     if device.type != "cuda":
         raise ValueError(f"{where}: tensors must be on a CUDA device, got {device}")
-    if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+    if stream is None:  # (torch.cuda.current_stream would cost 2 us, as much as the launch)
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
     else:
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
@@ -672,21 +674,24 @@ def state_cache(n_slots: int, state_shape, fmt: str = "e4m3", device="cuda"):
 def _state_cache_call(name, states, cache, scales, state_slots, cache_slots, stream):
     import torch
     dev = states.device
-    fmt = {torch.float8_e4m3fn: STATE_E4M3, torch.int8: STATE_INT8}.get(cache.dtype)
-    if fmt is None:
-        raise ValueError(f"cache must be float8_e4m3fn or int8, got {cache.dtype}")
-    if states.dim() < 2 or states.shape[-1] % 32 != 0:
+    kind = cache.dtype
+    if kind is not torch.float8_e4m3fn and kind is not torch.int8:
+        raise ValueError(f"cache must be float8_e4m3fn or int8, got {kind}")
+    fmt = STATE_INT8 if kind is torch.int8 else STATE_E4M3
+    n, *shape = states.shape
+    if not shape or shape[-1] % 32 != 0:
         raise ValueError(f"states must be [n, ..., a multiple of 32], got {tuple(states.shape)}")
-    shape = tuple(states.shape[1:])
-    ps = _check_dense(states, "states", torch.float32, dev, (states.shape[0], *shape))
-    pc = _check_dense(cache, "cache", cache.dtype, dev, (cache.shape[0], *shape))
-    pf = _check_dense(scales, "scales", torch.uint8, dev, (cache.shape[0], *shape[:-1], shape[-1] // 32))
-    count = len(state_slots if state_slots is not None else cache_slots if cache_slots is not None else states)
+    places = cache.shape[0]
+    ps = _check_dense(states, "states", torch.float32, dev, (n, *shape))
+    pc = _check_dense(cache, "cache", kind, dev, (places, *shape))
+    pf = _check_dense(scales, "scales", torch.uint8, dev, (places, *shape[:-1], shape[-1] // 32))
+    slots = state_slots if state_slots is not None else cache_slots
+    count = n if slots is None else slots.shape[0]
     a = StateCacheArgs(
         fmt, math.prod(shape), count,
         None if state_slots is None else _check_dense(state_slots, "state_slots", torch.int32, dev, (count,)),
         None if cache_slots is None else _check_dense(cache_slots, "cache_slots", torch.int32, dev, (count,)),
-        states.shape[0], cache.shape[0], ps, pc, pf)
+        n, places, ps, pc, pf)
     _call(getattr(load(), name), name, dev, stream, (), ctypes.byref(a))
 
 
