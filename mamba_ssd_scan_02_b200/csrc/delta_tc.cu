@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // rho_j 2^{cs_C - cs_j}, into its operand
     Ring<kDeep> r;
     for (int c = 0; c < nck; ++c, r.next()) {
-      const bool ok = wait2(BAR_M, c);
+      bool ok = wait(BAR_VG + r.at, r.parity);  // the factors
+      ok = wait2(BAR_M, c) && ok;
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const float4 *f = reinterpret_cast<const float4 *>(smem + OFF_VG + r.at * kVG + OFF_END);

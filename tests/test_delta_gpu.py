@@ -249,6 +249,33 @@ def test_streams_graphs_and_repeats(cuda_lib, kernel):
     assert none is None and torch.equal(y0, y2)
 
 
+@pytest.mark.parametrize("kernel", [SIMT, TENSOR])
+def test_a_full_machine_gives_equal_bits(cuda_lib, kernel):
+    """Many sequences at once, on every SM: the same bits whatever the workspace held and whatever the L2
+    cache holds.  On the tensor cores each sequence has the bits of its own call, too (in fp32 a small call
+    sums a row over eight lanes and a large one over four)."""
+    import torch
+    cfg = ref.config(nheads=64, ngroups=8)
+    r = np.random.default_rng(5)
+    cu = np.concatenate([[0], np.cumsum(r.integers(1, 500, 24))]).tolist()
+    g = on_gpu(ref.inputs(cfg, cu[-1], len(cu) - 1, seed=1))
+    n = cuda_lib.delta_varlen_workspace_size(cfg, cu, kernel)
+    flood = torch.empty(1 << 26, device="cuda")
+    first = None
+    for i in range(12):
+        if i % 3 == 1:
+            flood.fill_(float(i))
+        ws = torch.full((max(n, 1),), 37 * i % 251, dtype=torch.uint8, device="cuda")
+        got = run_packed(cuda_lib, cfg, g, cu, True, kernel, workspace=ws)
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got)), i
+    for i in (0, 7, 23) if kernel == TENSOR else ():
+        part = {k: v[cu[i]:cu[i + 1]] if k in ("q", "k", "v", "dt", "b") else v for k, v in g.items()}
+        part["h0"] = g["h0"][i:i + 1]
+        y, h = run_packed(cuda_lib, cfg, part, [0, cu[i + 1] - cu[i]], True, kernel)
+        assert torch.equal(y, first[0][cu[i]:cu[i + 1]]) and torch.equal(h[0], first[1][i]), i
+
+
 def test_decode_graph(cuda_lib):
     """Captured decode steps over a pool, with the slots changed between replays."""
     import torch
