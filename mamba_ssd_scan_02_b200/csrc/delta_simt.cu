@@ -1,17 +1,22 @@
-// delta_simt.cu -- the gated delta rule token by token in fp32: the decode step, short prefills and
-// fp32 inputs.
+// delta_simt.cu -- the gated delta rule in fp32: the decode step, short prefills and fp32 inputs.
 //
 // Per head and token, with S the P x N state and k^, q^ the normalised key and scaled query:
 //   u = beta (v - alpha S k^),  y = alpha S q^ + u (k^.q^),  S <- alpha S + u k^^T.
 // y is S_t q^ written with the old state, so both products with S come from one pass over it and
-// one reduction, and k^.q^ is a scalar per token: the chain from token to token is one dot
-// product, one reduction over a few lanes and one multiply-add.
+// one reduction, and k^.q^ is a scalar per token.
 //
 // The rows of S are independent given k^, so LPR lanes hold a row (N / LPR elements each, in
-// registers for the whole call) and a warp holds 32 / LPR rows.  The tokens are taken in tiles:
-// the CTA reads a tile's q, k, v, dt and b into registers while it works on the tile before,
-// then normalises q and k and puts all of it into shared memory, from which the token loop
-// reads with broadcasts.
+// registers for the whole call) and a warp holds 32 / LPR rows.
+//
+// A sequence is taken four tokens at a time.  With g_j = alpha_0 .. alpha_j and D_ij = alpha_{i+1} .. alpha_j,
+//   u_j = beta_j (v_j - g_j S k_j - sum_{i<j} D_ij (k_i.k_j) u_i)
+//   y_j = g_j S q_j + sum_{i<=j} D_ij (k_i.q_j) u_i
+//   S  <- g_3 S + sum_j D_j3 u_j k_j^T,
+// so eight products with the old S share one reduction over the lanes, and the chain from token to token
+// is a quarter of a dot product, a reduction and an update, plus a triangular solve in scalars.  (Token by
+// token the reductions alone held it at 630 clocks a token.)  The scalars (D, k_i.k_j, k_i.q_j) are the
+// same for all rows: a warp works them out per four tokens, when the tile of 16 tokens that the CTA has
+// read into registers during the tile before is normalised and put into shared memory.
 #include "common.cuh"
 #include "delta_plan.h"
 #include "plan.h"
@@ -30,176 +35,371 @@ __device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&v)[4]) {
   v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
 
-// kDecode: one token per row, the state in place in a pool; else whole sequences.
-template <typename T, int LPR, int WARPS, int TT, bool kDecode>
+__device__ __forceinline__ float step_of(float raw, float bias, const DeltaPlan &p) {
+  float d = raw + bias;
+  if (p.softplus) d = d > 20.f ? d : log1pf(expf(d));
+  return d < p.dt_min ? p.dt_min : d > p.dt_max ? p.dt_max : d;  // (a NaN stays)
+}
+__device__ __forceinline__ float beta_of(float raw, const DeltaPlan &p) {
+  return p.beta_scale * (p.beta_sigmoid ? 1.f / (1.f + expf(-raw)) : raw);
+}
+
+// What four tokens share, whatever the row; j the later token, i the earlier
+struct Four {
+  float g[4], beta[4], end[4];  // g_j, beta_j, D_j3
+  float kk[4][4];               // [j][i]: beta_j D_ij k_i.k_j, i < j
+  float kq[4][4];               // [j][i]: D_ij k_i.q_j, i <= j
+};
+__device__ __forceinline__ constexpr int pair_at(int i, int j) { return j * (j + 1) / 2 + i; }  // i <= j
+
+template <typename T, int LPR, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32) delta_recurrent_kernel(const DeltaPlan p) {
+  constexpr int TT = 16;                // tokens of a tile
   constexpr int R = WARPS * 32 / LPR;   // state rows of this CTA
   constexpr int E4 = kDState / LPR / 4; // float4s of a row per lane
   constexpr int NT = WARPS * 32;
-  constexpr int TPW = (TT + WARPS - 1) / WARPS;  // tokens of a tile that a warp normalises
-  constexpr int VPT = (TT * R + NT - 1) / NT;    // v elements of a tile per thread
-  constexpr int NB = kDecode ? 1 : 2;
-  __shared__ __align__(16) float sq[NB][TT][kDState], sk[NB][TT][kDState];
-  __shared__ float sv[NB][TT][R];
-  __shared__ float s_alpha[NB][TT], s_beta[NB][TT], s_kq[NB][TT];
+  constexpr int VPT = TT * R / NT;      // v elements of a tile per thread
+  constexpr int VP = TT + 4;
+  constexpr bool kHold = LPR == 8;      // keep the four keys in registers from the products to the update
+  __shared__ __align__(16) float sq[2][TT][kDState], sk[2][TT][kDState];
+  __shared__ __align__(16) float sv[2][R][VP];
+  __shared__ __align__(16) Four s_four[2][TT / 4];
+  __shared__ float s_dot[TT / 4][24];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int blocks_per_head = p.P / R;
   const int h = blockIdx.x / blocks_per_head, row0 = (blockIdx.x % blocks_per_head) * R;
   const int seq = p.order ? p.order[blockIdx.y] : (int)blockIdx.y;
   const int g = h / p.hpg;
-  const int len = kDecode ? 1 : seq_len(p.cu, seq, p.L);
-  const long long base = kDecode ? (long long)seq : seq_base(p.cu, seq, p.L);
+  const int len = seq_len(p.cu, seq, p.L);
+  const long long base = seq_base(p.cu, seq, p.L);
   const int r = warp * (32 / LPR) + lane / LPR, s = lane % LPR;
+  const long long soff = (((long long)seq * p.H + h) * p.P + row0 + r) * kDState + 4 * s;
 
-  long long state_idx = seq;
-  bool skip = false;
-  if (kDecode && p.slots) {
-    const int own = p.slots[seq];
-    bool twice = false;  // an earlier row of the batch has this slot
-    for (int j = tid; j < seq; j += NT) twice |= p.slots[j] == own;
-    skip = own < 0;
-    const bool bad = own >= p.n_slots || __syncthreads_or(twice && !skip);
-    if (bad && !skip && tid == 0) latch_error(p.err, (int)SSD_ERR_DEVICE_BOUNDS);
-    skip |= bad;
-    if (skip) return;
-    state_idx = own;
-  }
-  const long long soff = ((state_idx * p.H + h) * p.P + row0 + r) * kDState + 4 * s;
-
-  float S[E4][4];
-  const float *src = kDecode ? p.h_final : p.h0;
+  float2 S[E4][2];
 #pragma unroll
   for (int j = 0; j < E4; ++j) {
-    if (src) {
-      load4(src + soff + 4 * LPR * j, S[j]);
-    } else {
-      S[j][0] = S[j][1] = S[j][2] = S[j][3] = 0.f;
-    }
+    const float4 x = p.h0 ? *reinterpret_cast<const float4 *>(p.h0 + soff + 4 * LPR * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+    S[j][0] = make_float2(x.x, x.y);
+    S[j][1] = make_float2(x.z, x.w);
   }
 
   const float A = p.A[h], bias = p.dt_bias[h];
-  const T *q = static_cast<const T *>(p.q) + g * kDState + 4 * lane;
-  const T *k = static_cast<const T *>(p.k) + g * kDState + 4 * lane;
-  const T *v = static_cast<const T *>(p.v) + h * p.P + row0;
-  const T *dt = static_cast<const T *>(p.dt) + h;
-  const T *bb = static_cast<const T *>(p.b) + h;
-  float rq[TPW][4], rk[TPW][4], rv[VPT], rdt = 0.f, rb = 0.f;
+  const T *q = static_cast<const T *>(p.q) + base * p.qs + g * kDState + 4 * lane;
+  const T *k = static_cast<const T *>(p.k) + base * p.ks + g * kDState + 4 * lane;
+  const T *v = static_cast<const T *>(p.v) + base * p.vs + h * p.P + row0;
+  const T *dt = static_cast<const T *>(p.dt) + base * p.ds + h;
+  const T *bb = static_cast<const T *>(p.b) + base * p.bs + h;
+  const bool stages = warp < TT / 4;  // four tokens each
+  float rq[4][4], rk[4][4], rv[VPT], rdt = 0.f, rb = 0.f;
 
-  auto fetch = [&](int t0) {  // this thread's part of the tile at t0, into registers
+  // This thread's part of the tile at t0, into registers.  Tokens after the last are loaded as the last.
+  auto fetch = [&](int t0) {
+    const int last = len - 1;
+    if (stages) {
 #pragma unroll
-    for (int i = 0; i < TPW; ++i) {
-      const int t = t0 + warp + i * WARPS;
-      if (warp + i * WARPS < TT && t < len) {
-        load4(q + (base + t) * p.qs, rq[i]);
-        load4(k + (base + t) * p.ks, rk[i]);
+      for (int i = 0; i < 4; ++i) {
+        const long long t = min(t0 + 4 * warp + i, last);
+        load4(q + t * p.qs, rq[i]);
+        load4(k + t * p.ks, rk[i]);
       }
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int at = tid + i * NT, t = t0 + at / R;
-      if (at < TT * R && t < len) rv[i] = io<T>::ld(v + (base + t) * p.vs + at % R);
-    }
-    if (tid < TT && t0 + tid < len) {
-      rdt = io<T>::ld(dt + (base + t0 + tid) * p.ds);
-      rb = io<T>::ld(bb + (base + t0 + tid) * p.bs);
-    }
-  };
-  auto stage = [&](int t0, int buf) {  // the fetched tile into shared memory
-#pragma unroll
-    for (int i = 0; i < TPW; ++i) {
-      const int at = warp + i * WARPS;
-      if (at < TT && t0 + at < len) {
-        float qq = 0.f, kk = 0.f, qk = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          qq = fmaf(rq[i][e], rq[i][e], qq);
-          kk = fmaf(rk[i][e], rk[i][e], kk);
-          qk = fmaf(rq[i][e], rk[i][e], qk);
-        }
-        float fq = p.q_scale, fk = 1.f;
-        if (p.qk_norm) {
-          fq *= 1.f / sqrtf(warp_sum(qq) + p.qk_eps);
-          fk = 1.f / sqrtf(warp_sum(kk) + p.qk_eps);
-        }
-        qk = warp_sum(qk);
-        *reinterpret_cast<float4 *>(&sq[buf][at][4 * lane]) =
-            make_float4(rq[i][0] * fq, rq[i][1] * fq, rq[i][2] * fq, rq[i][3] * fq);
-        *reinterpret_cast<float4 *>(&sk[buf][at][4 * lane]) =
-            make_float4(rk[i][0] * fk, rk[i][1] * fk, rk[i][2] * fk, rk[i][3] * fk);
-        if (lane == 0) s_kq[buf][at] = qk * fq * fk;
-      }
+      const long long t = min(t0 + 4 * warp + (lane & 3), last);
+      rdt = io<T>::ld(dt + t * p.ds);
+      rb = io<T>::ld(bb + t * p.bs);
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int at = tid + i * NT;
-      if (at < TT * R) sv[buf][at / R][at % R] = rv[i];
+      rv[i] = io<T>::ld(v + (long long)min(t0 + at / R, last) * p.vs + at % R);
     }
-    if (tid < TT) {
-      float d = rdt + bias;
-      if (p.softplus) d = d > 20.f ? d : log1pf(expf(d));
-      d = fminf(fmaxf(d, p.dt_min), p.dt_max);
-      s_alpha[buf][tid] = expf(A * d);
-      s_beta[buf][tid] = p.beta_scale * (p.beta_sigmoid ? 1.f / (1.f + expf(-rb)) : rb);
+  };
+  // The fetched tile into shared memory.  Tokens after the last: zeros, no decay.
+  auto stage = [&](int t0, int buf) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int at = tid + i * NT;
+      sv[buf][at % R][at / R] = t0 + at / R < len ? rv[i] : 0.f;
+    }
+    if (!stages) return;
+    const int first = t0 + 4 * warp;
+    float x[24];  // k_i.k_j (i <= j), k_i.q_j (i <= j), q_j.q_j
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (first + j >= len)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rk[j][e] = rq[j][e] = 0.f;
+#pragma unroll
+      for (int i = 0; i <= j; ++i) {
+        float kk = 0.f, kq = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          kk = fmaf(rk[i][e], rk[j][e], kk);
+          kq = fmaf(rk[i][e], rq[j][e], kq);
+        }
+        x[pair_at(i, j)] = kk;
+        x[10 + pair_at(i, j)] = kq;
+      }
+      float qq = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) qq = fmaf(rq[j][e], rq[j][e], qq);
+      x[20 + j] = qq;
+    }
+    // all 24 sums over the warp at once: at each of three levels a lane hands half of them over
+#pragma unroll
+    for (int o = 16, n = 12; o >= 4; o >>= 1, n >>= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float give = up ? x[i] : x[i + n];
+        x[i] = (up ? x[i + n] : x[i]) + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    }
+#pragma unroll
+    for (int o = 2; o >= 1; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+    if ((lane & 3) < 3) s_dot[warp][3 * (lane >> 2) + (lane & 3)] = (lane & 3) == 0 ? x[0] : (lane & 3) == 1 ? x[1] : x[2];
+    __syncwarp();
+    const float *dot = s_dot[warp];
+    const int i = lane & 3, j = lane >> 2 & 3;  // (lanes 16-31 as lanes 0-15)
+    float fk_j = 1.f, fq_j = p.q_scale;
+    if (p.qk_norm) {
+      fk_j = 1.f / sqrtf(dot[pair_at(j, j)] + p.qk_eps);
+      fq_j *= 1.f / sqrtf(dot[20 + j] + p.qk_eps);
+    }
+    const float fk_i = __shfl_sync(0xffffffffu, fk_j, 4 * i);
+    const bool live = first + i < len;  // (rdt and rb are token i's)
+    const float alpha = live ? expf(A * step_of(rdt, bias, p)) : 1.f;
+    const float beta = live ? beta_of(rb, p) : 0.f;
+    const float beta_j = __shfl_sync(0xffffffffu, beta, j);
+    float a[4], gj = 1.f, d = 1.f;
+#pragma unroll
+    for (int l = 0; l < 4; ++l) {
+      a[l] = __shfl_sync(0xffffffffu, alpha, l);
+      if (l <= j) gj *= a[l];
+      if (l > i && l <= j) d *= a[l];
+    }
+    Four &f = s_four[buf][warp];
+    if (lane < 16) {
+      const int at = i <= j ? pair_at(i, j) : 0;
+      f.kk[j][i] = i < j ? beta_j * d * fk_i * fk_j * dot[at] : 0.f;
+      f.kq[j][i] = i <= j ? d * fk_i * fq_j * dot[10 + at] : 0.f;
+      if (i == 0) f.g[j] = gj;
+      if (i == 0) f.beta[j] = beta_j;
+      if (j == 3) f.end[i] = d;
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const float fk = __shfl_sync(0xffffffffu, fk_j, 4 * t), fq = __shfl_sync(0xffffffffu, fq_j, 4 * t);
+      *reinterpret_cast<float4 *>(&sk[buf][4 * warp + t][4 * lane]) = make_float4(rk[t][0] * fk, rk[t][1] * fk, rk[t][2] * fk, rk[t][3] * fk);
+      *reinterpret_cast<float4 *>(&sq[buf][4 * warp + t][4 * lane]) = make_float4(rq[t][0] * fq, rq[t][1] * fq, rq[t][2] * fq, rq[t][3] * fq);
     }
   };
 
   T *y = static_cast<T *>(p.y);
-  const long long yoff = (long long)h * p.P + row0 + r;
+  const long long yoff = base * p.ys + (long long)h * p.P + row0 + r;
   if (len > 0) fetch(0);
-  for (int t0 = 0, buf = 0; t0 < len; t0 += TT, buf ^= NB - 1) {
+  for (int t0 = 0, buf = 0; t0 < len; t0 += TT, buf ^= 1) {
     stage(t0, buf);
     __syncthreads();
-    if (!kDecode && t0 + TT < len) fetch(t0 + TT);
-    const int nt = min(TT, len - t0);
-    for (int t = 0; t < nt; ++t) {
-      float kv[E4][4], dk[2] = {0.f, 0.f}, dq[2] = {0.f, 0.f};
+    if (t0 + TT < len) fetch(t0 + TT);
+    const int blocks = (min(TT, len - t0) + 3) / 4;
+#pragma unroll 1
+    for (int b = 0; b < blocks; ++b) {
+      const Four &f = s_four[buf][b];
+      const float *kp = &sk[buf][4 * b][4 * s], *qp = &sq[buf][4 * b][4 * s];
+      float2 kv[kHold ? 4 : 1][E4][2], acc[8];
 #pragma unroll
-      for (int j = 0; j < E4; ++j) {
-        load4(&sk[buf][t][4 * (j * LPR + s)], kv[j]);
-        float qv[4];
-        load4(&sq[buf][t][4 * (j * LPR + s)], qv);
+      for (int j = 0; j < 8; ++j) acc[j] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          dk[e & 1] = fmaf(S[j][e], kv[j][e], dk[e & 1]);
-          dq[e & 1] = fmaf(S[j][e], qv[e], dq[e & 1]);
+      for (int e = 0; e < E4; ++e)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 x = *reinterpret_cast<const float4 *>(kp + j * kDState + 4 * LPR * e);
+          const float4 z = *reinterpret_cast<const float4 *>(qp + j * kDState + 4 * LPR * e);
+          const float2 x0 = make_float2(x.x, x.y), x1 = make_float2(x.z, x.w);
+          acc[j] = __ffma2_rn(S[e][0], x0, acc[j]);
+          acc[j] = __ffma2_rn(S[e][1], x1, acc[j]);
+          acc[4 + j] = __ffma2_rn(S[e][0], make_float2(z.x, z.y), acc[4 + j]);
+          acc[4 + j] = __ffma2_rn(S[e][1], make_float2(z.z, z.w), acc[4 + j]);
+          if (kHold) {
+            kv[kHold ? j : 0][e][0] = x0;
+            kv[kHold ? j : 0][e][1] = x1;
+          }
+        }
+      float x[8];  // S k_j, S q_j: their sums over the row's lanes, handed over like those of stage()
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = acc[j].x + acc[j].y;
+#pragma unroll
+      for (int o = LPR / 2, n = 4; o > 0; o >>= 1, n >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+          const float give = up ? x[j] : x[j + n];
+          x[j] = (up ? x[j + n] : x[j]) + __shfl_xor_sync(0xffffffffu, give, o);
         }
       }
-      float dk_ = dk[0] + dk[1], dq_ = dq[0] + dq[1];
+      constexpr int X = 8 / LPR;  // sums that a lane ends with: number X s ..
+      const float4 g4 = *reinterpret_cast<const float4 *>(f.g), b4 = *reinterpret_cast<const float4 *>(f.beta);
+      const float4 v4 = *reinterpret_cast<const float4 *>(&sv[buf][r][4 * b]);
+      float dk[4], u[4];
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) {
-        dk_ += __shfl_xor_sync(0xffffffffu, dk_, o);
-        dq_ += __shfl_xor_sync(0xffffffffu, dq_, o);
+      for (int j = 0; j < 4; ++j) dk[j] = __shfl_sync(0xffffffffu, x[j % X], (lane & ~(LPR - 1)) | (j / X));
+      u[0] = b4.x * fmaf(-g4.x, dk[0], v4.x);
+      u[1] = fmaf(-f.kk[1][0], u[0], b4.y * fmaf(-g4.y, dk[1], v4.y));
+      u[2] = b4.z * fmaf(-g4.z, dk[2], v4.z);
+      u[3] = b4.w * fmaf(-g4.w, dk[3], v4.w);
+      u[2] = fmaf(-f.kk[2][1], u[1], fmaf(-f.kk[2][0], u[0], u[2]));
+      u[3] = fmaf(-f.kk[3][2], u[2], fmaf(-f.kk[3][1], u[1], fmaf(-f.kk[3][0], u[0], u[3])));
+      if (s >= LPR / 2) {
+#pragma unroll
+        for (int c = 0; c < X; ++c) {
+          const int j = X * (s - LPR / 2) + c, t = t0 + 4 * b + j;
+          const float4 kq = *reinterpret_cast<const float4 *>(f.kq[j]);
+          // (what comes after token j is left out, not multiplied by zero: it may be NaN)
+          float o = fmaf(kq.x, u[0], f.g[j] * x[c]);
+          if (j >= 1) o = fmaf(kq.y, u[1], o);
+          if (j >= 2) o = fmaf(kq.z, u[2], o);
+          if (j >= 3) o = fmaf(kq.w, u[3], o);
+          const long long yo = (long long)t * p.ys + yoff;
+          if (t < len && in_bounds(yo, p.y_extent, p.err)) io<T>::st(y + yo, o);
+        }
       }
-      const float alpha = s_alpha[buf][t];
-      const float u = s_beta[buf][t] * (sv[buf][t][r] - alpha * dk_);
-      if (s == 0) {
-        const long long yo = (base + t0 + t) * p.ys + yoff;
-        if (in_bounds(yo, p.y_extent, p.err)) io<T>::st(y + yo, fmaf(u, s_kq[buf][t], alpha * dq_));
+      const float4 end = *reinterpret_cast<const float4 *>(f.end);
+      const float2 ge = make_float2(g4.w, g4.w);
+      const float w[4] = {u[0] * end.x, u[1] * end.y, u[2] * end.z, u[3] * end.w};
+#pragma unroll
+      for (int e = 0; e < E4; ++e) {
+        S[e][0] = __fmul2_rn(S[e][0], ge);
+        S[e][1] = __fmul2_rn(S[e][1], ge);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 x0, x1;
+          if (kHold) {
+            x0 = kv[kHold ? j : 0][e][0];
+            x1 = kv[kHold ? j : 0][e][1];
+          } else {
+            const float4 z = *reinterpret_cast<const float4 *>(kp + j * kDState + 4 * LPR * e);
+            x0 = make_float2(z.x, z.y);
+            x1 = make_float2(z.z, z.w);
+          }
+          const float2 w2 = make_float2(w[j], w[j]);
+          S[e][0] = __ffma2_rn(w2, x0, S[e][0]);
+          S[e][1] = __ffma2_rn(w2, x1, S[e][1]);
+        }
       }
-#pragma unroll
-      for (int j = 0; j < E4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[j][e] = fmaf(u, kv[j][e], alpha * S[j][e]);
     }
   }
   if (p.h_final) {
 #pragma unroll
     for (int j = 0; j < E4; ++j)
       if (in_bounds(soff + 4 * LPR * j + 3, p.state_extent, p.err))
-        *reinterpret_cast<float4 *>(p.h_final + soff + 4 * LPR * j) =
-            make_float4(S[j][0], S[j][1], S[j][2], S[j][3]);
+        *reinterpret_cast<float4 *>(p.h_final + soff + 4 * LPR * j) = make_float4(S[j][0].x, S[j][0].y, S[j][1].x, S[j][1].y);
   }
 }
 
-template <typename T, bool kDecode>
-cudaError_t launch(const DeltaPlan &p, cudaStream_t s) {
-  constexpr int TT = kDecode ? 1 : 16;
-  // 16 rows per CTA spread a small call over more SMs
-  if ((long long)p.B * p.H * p.P <= 64 * 2 * 148) {
-    delta_recurrent_kernel<T, 8, 4, TT, kDecode><<<dim3(p.H * p.P / 16, p.B), 128, 0, s>>>(p);
-  } else {
-    delta_recurrent_kernel<T, 4, 8, TT, kDecode><<<dim3(p.H * p.P / 64, p.B), 256, 0, s>>>(p);
+// One token per row, the state in place in a pool.
+template <typename T, int LPR, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) delta_decode_kernel(const DeltaPlan p) {
+  constexpr int R = WARPS * 32 / LPR;   // state rows of this CTA
+  constexpr int E4 = kDState / LPR / 4; // float4s of a row per lane
+  constexpr int NT = WARPS * 32;
+  __shared__ __align__(16) float sq[kDState], sk[kDState];
+  __shared__ float s_kq;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int blocks_per_head = p.P / R;
+  const int h = blockIdx.x / blocks_per_head, row0 = (blockIdx.x % blocks_per_head) * R;
+  const int g = h / p.hpg;
+  const long long seq = blockIdx.y;
+  const int r = warp * (32 / LPR) + lane / LPR, s = lane % LPR;
+
+  long long state_idx = seq;
+  if (p.slots) {
+    const int own = p.slots[seq];
+    if (own < 0) return;
+    bool twice = false;  // an earlier row of the batch has this slot
+    for (int j = tid; j < seq; j += NT) twice |= p.slots[j] == own;
+    if (__syncthreads_or(twice) || own >= p.n_slots) {
+      if (tid == 0) latch_error(p.err, (int)SSD_ERR_DEVICE_BOUNDS);
+      return;
+    }
+    state_idx = own;
   }
+  const long long soff = ((state_idx * p.H + h) * p.P + row0 + r) * kDState + 4 * s;
+  float S[E4][4];
+#pragma unroll
+  for (int j = 0; j < E4; ++j) load4(p.h_final + soff + 4 * LPR * j, S[j]);
+  const float vr = io<T>::ld(static_cast<const T *>(p.v) + seq * p.vs + h * p.P + row0 + r);
+  const float rdt = io<T>::ld(static_cast<const T *>(p.dt) + seq * p.ds + h);
+  const float rb = io<T>::ld(static_cast<const T *>(p.b) + seq * p.bs + h);
+  const float A = p.A[h], bias = p.dt_bias[h];
+  if (warp == 0) {
+    float rq[4], rk[4];
+    load4(static_cast<const T *>(p.q) + seq * p.qs + g * kDState + 4 * lane, rq);
+    load4(static_cast<const T *>(p.k) + seq * p.ks + g * kDState + 4 * lane, rk);
+    float qq = 0.f, kk = 0.f, qk = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      qq = fmaf(rq[e], rq[e], qq);
+      kk = fmaf(rk[e], rk[e], kk);
+      qk = fmaf(rq[e], rk[e], qk);
+    }
+    float fq = p.q_scale, fk = 1.f;
+    if (p.qk_norm) {
+      fq *= 1.f / sqrtf(warp_sum(qq) + p.qk_eps);
+      fk = 1.f / sqrtf(warp_sum(kk) + p.qk_eps);
+    }
+    qk = warp_sum(qk);
+    *reinterpret_cast<float4 *>(&sq[4 * lane]) = make_float4(rq[0] * fq, rq[1] * fq, rq[2] * fq, rq[3] * fq);
+    *reinterpret_cast<float4 *>(&sk[4 * lane]) = make_float4(rk[0] * fk, rk[1] * fk, rk[2] * fk, rk[3] * fk);
+    if (lane == 0) s_kq = qk * fq * fk;
+  }
+  const float alpha = expf(A * step_of(rdt, bias, p)), beta = beta_of(rb, p);
+  __syncthreads();
+  float kv[E4][4], dk[2] = {0.f, 0.f}, dq[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < E4; ++j) {
+    load4(&sk[4 * (j * LPR + s)], kv[j]);
+    float qv[4];
+    load4(&sq[4 * (j * LPR + s)], qv);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      dk[e & 1] = fmaf(S[j][e], kv[j][e], dk[e & 1]);
+      dq[e & 1] = fmaf(S[j][e], qv[e], dq[e & 1]);
+    }
+  }
+  float dk_ = dk[0] + dk[1], dq_ = dq[0] + dq[1];
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) {
+    dk_ += __shfl_xor_sync(0xffffffffu, dk_, o);
+    dq_ += __shfl_xor_sync(0xffffffffu, dq_, o);
+  }
+  const float u = beta * (vr - alpha * dk_);
+  if (s == 0) {
+    const long long yo = seq * p.ys + (long long)h * p.P + row0 + r;
+    if (in_bounds(yo, p.y_extent, p.err)) io<T>::st(static_cast<T *>(p.y) + yo, fmaf(u, s_kq, alpha * dq_));
+  }
+#pragma unroll
+  for (int j = 0; j < E4; ++j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[j][e] = fmaf(u, kv[j][e], alpha * S[j][e]);
+    if (in_bounds(soff + 4 * LPR * j + 3, p.state_extent, p.err))
+      *reinterpret_cast<float4 *>(p.h_final + soff + 4 * LPR * j) = make_float4(S[j][0], S[j][1], S[j][2], S[j][3]);
+  }
+}
+
+// 16 rows per CTA spread a small call over more SMs
+bool is_small(const DeltaPlan &p) { return (long long)p.B * p.H * p.P <= 64 * 2 * 148; }
+
+template <typename T>
+cudaError_t launch_recurrent(const DeltaPlan &p, cudaStream_t s) {
+  if (is_small(p)) delta_recurrent_kernel<T, 8, 4><<<dim3(p.H * p.P / 16, p.B), 128, 0, s>>>(p);
+  else delta_recurrent_kernel<T, 4, 8><<<dim3(p.H * p.P / 64, p.B), 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_decode(const DeltaPlan &p, cudaStream_t s) {
+  if (is_small(p)) delta_decode_kernel<T, 8, 4><<<dim3(p.H * p.P / 16, p.B), 128, 0, s>>>(p);
+  else delta_decode_kernel<T, 4, 8><<<dim3(p.H * p.P / 64, p.B), 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -213,10 +413,10 @@ __global__ void put_ints_kernel(int *dst, const __grid_constant__ Ints src, int 
 }  // namespace
 
 cudaError_t launch_delta_recurrent(const DeltaPlan &p, cudaStream_t s) {
-  return p.bf16 ? launch<__nv_bfloat16, false>(p, s) : launch<float, false>(p, s);
+  return p.bf16 ? launch_recurrent<__nv_bfloat16>(p, s) : launch_recurrent<float>(p, s);
 }
 cudaError_t launch_delta_decode(const DeltaPlan &p, cudaStream_t s) {
-  return p.bf16 ? launch<__nv_bfloat16, true>(p, s) : launch<float, true>(p, s);
+  return p.bf16 ? launch_decode<__nv_bfloat16>(p, s) : launch_decode<float>(p, s);
 }
 
 cudaError_t launch_put_ints(int *dst, const int *host, int n, cudaStream_t s) {
