@@ -5,18 +5,19 @@
 // y is S_t q^ written with the old state, so both products with S come from one pass over it and
 // one reduction, and k^.q^ is a scalar per token.
 //
-// The rows of S are independent given k^, so LPR lanes hold a row (N / LPR elements each, in
-// registers for the whole call) and a warp holds 32 / LPR rows.
+// The rows of S are independent given k^, so a few lanes hold a row (in registers for the whole call), a warp
+// several rows.
 //
 // A sequence is taken four tokens at a time.  With g_j = alpha_0 .. alpha_j and D_ij = alpha_{i+1} .. alpha_j,
 //   u_j = beta_j (v_j - g_j S k_j - sum_{i<j} D_ij (k_i.k_j) u_i)
 //   y_j = g_j S q_j + sum_{i<=j} D_ij (k_i.q_j) u_i
 //   S  <- g_3 S + sum_j D_j3 u_j k_j^T,
-// so eight products with the old S share one reduction over the lanes, and the chain from token to token
-// is a quarter of a dot product, a reduction and an update, plus a triangular solve in scalars.  (Token by
-// token the reductions alone held it at 630 clocks a token.)  The scalars (D, k_i.k_j, k_i.q_j) are the
-// same for all rows: a warp works them out per four tokens, when the tile of 16 tokens that the CTA has
-// read into registers during the tile before is normalised and put into shared memory.
+// so eight products with the old S share one reduction over the lanes of a row, and the chain from token to
+// token is a quarter of a dot product, a reduction and an update, plus a triangular solve in scalars (about
+// 250 clocks a token; token by token it was 630).  The scalars (D, k_i.k_j, k_i.q_j) are the same for all rows:
+// four warps of the CTA work them out for a tile of 16 tokens, normalise q and k and put it all into shared
+// memory, while the others run the tile before; their loads run two tiles ahead.  What bounds it then is
+// shared memory: a warp reads 8 vectors for 4 rows.  256 tokens x 8 heads in fp32: 31 us.
 #include "common.cuh"
 #include "delta_plan.h"
 #include "plan.h"
@@ -52,15 +53,18 @@ struct Four {
 };
 __device__ __forceinline__ constexpr int pair_at(int i, int j) { return j * (j + 1) / 2 + i; }  // i <= j
 
-template <typename T, int LPR, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) delta_recurrent_kernel(const DeltaPlan p) {
-  constexpr int TT = 16;                // tokens of a tile
-  constexpr int R = WARPS * 32 / LPR;   // state rows of this CTA
+// Warps 0-3 stage a tile, four tokens each, while warps 4 .. 3 + CW run the tokens of the tile before.
+constexpr int kStageWarps = 4;
+
+template <typename T, int CW>
+__global__ void __launch_bounds__((kStageWarps + CW) * 32, 1) delta_recurrent_kernel(const DeltaPlan p) {
+  constexpr int LPR = 8;                // lanes of a row: as many as there are products per reduction
+  constexpr int TT = 4 * kStageWarps;   // tokens of a tile
+  constexpr int R = CW * 32 / LPR;      // state rows of this CTA
   constexpr int E4 = kDState / LPR / 4; // float4s of a row per lane
-  constexpr int NT = WARPS * 32;
-  constexpr int VPT = TT * R / NT;      // v elements of a tile per thread
+  constexpr int NT = kStageWarps * 32;
+  constexpr int VPT = (TT * R + NT - 1) / NT;  // v elements of a tile per staging thread
   constexpr int VP = TT + 4;
-  constexpr bool kHold = LPR == 8;      // keep the four keys in registers from the products to the update
   __shared__ __align__(16) float sq[2][TT][kDState], sk[2][TT][kDState];
   __shared__ __align__(16) float sv[2][R][VP];
   __shared__ __align__(16) Four s_four[2][TT / 4];
@@ -72,54 +76,42 @@ __global__ void __launch_bounds__(WARPS * 32) delta_recurrent_kernel(const Delta
   const int g = h / p.hpg;
   const int len = seq_len(p.cu, seq, p.L);
   const long long base = seq_base(p.cu, seq, p.L);
-  const int r = warp * (32 / LPR) + lane / LPR, s = lane % LPR;
-  const long long soff = (((long long)seq * p.H + h) * p.P + row0 + r) * kDState + 4 * s;
-
-  float2 S[E4][2];
-#pragma unroll
-  for (int j = 0; j < E4; ++j) {
-    const float4 x = p.h0 ? *reinterpret_cast<const float4 *>(p.h0 + soff + 4 * LPR * j) : make_float4(0.f, 0.f, 0.f, 0.f);
-    S[j][0] = make_float2(x.x, x.y);
-    S[j][1] = make_float2(x.z, x.w);
-  }
-
   const float A = p.A[h], bias = p.dt_bias[h];
   const T *q = static_cast<const T *>(p.q) + base * p.qs + g * kDState + 4 * lane;
   const T *k = static_cast<const T *>(p.k) + base * p.ks + g * kDState + 4 * lane;
   const T *v = static_cast<const T *>(p.v) + base * p.vs + h * p.P + row0;
   const T *dt = static_cast<const T *>(p.dt) + base * p.ds + h;
   const T *bb = static_cast<const T *>(p.b) + base * p.bs + h;
-  const bool stages = warp < TT / 4;  // four tokens each
-  float rq[4][4], rk[4][4], rv[VPT], rdt = 0.f, rb = 0.f;
+  struct Tile {
+    float rq[4][4], rk[4][4], rv[VPT], rdt, rb;
+  } even, odd;  // two tiles on the way from memory
 
   // This thread's part of the tile at t0, into registers.  Tokens after the last are loaded as the last.
-  auto fetch = [&](int t0) {
+  auto fetch = [&](Tile &x, int t0) {
     const int last = len - 1;
-    if (stages) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long long t = min(t0 + 4 * warp + i, last);
-        load4(q + t * p.qs, rq[i]);
-        load4(k + t * p.ks, rk[i]);
-      }
-      const long long t = min(t0 + 4 * warp + (lane & 3), last);
-      rdt = io<T>::ld(dt + t * p.ds);
-      rb = io<T>::ld(bb + t * p.bs);
+    for (int i = 0; i < 4; ++i) {
+      const long long t = min(t0 + 4 * warp + i, last);
+      load4(q + t * p.qs, x.rq[i]);
+      load4(k + t * p.ks, x.rk[i]);
     }
+    const long long td = min(t0 + 4 * warp + (lane & 3), last);
+    x.rdt = io<T>::ld(dt + td * p.ds);
+    x.rb = io<T>::ld(bb + td * p.bs);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int at = tid + i * NT;
-      rv[i] = io<T>::ld(v + (long long)min(t0 + at / R, last) * p.vs + at % R);
+      const int at = min(tid + i * NT, TT * R - 1);
+      x.rv[i] = io<T>::ld(v + (long long)min(t0 + at / R, last) * p.vs + at % R);
     }
   };
   // The fetched tile into shared memory.  Tokens after the last: zeros, no decay.
-  auto stage = [&](int t0, int buf) {
+  auto stage = [&](Tile &tile, int t0, int buf) {
+    float(&rq)[4][4] = tile.rq, (&rk)[4][4] = tile.rk;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int at = tid + i * NT;
-      sv[buf][at % R][at / R] = t0 + at / R < len ? rv[i] : 0.f;
+      if (at < TT * R) sv[buf][at % R][at / R] = t0 + at / R < len ? tile.rv[i] : 0.f;
     }
-    if (!stages) return;
     const int first = t0 + 4 * warp;
     float x[24];  // k_i.k_j (i <= j), k_i.q_j (i <= j), q_j.q_j
 #pragma unroll
@@ -168,8 +160,8 @@ __global__ void __launch_bounds__(WARPS * 32) delta_recurrent_kernel(const Delta
     }
     const float fk_i = __shfl_sync(0xffffffffu, fk_j, 4 * i);
     const bool live = first + i < len;  // (rdt and rb are token i's)
-    const float alpha = live ? expf(A * step_of(rdt, bias, p)) : 1.f;
-    const float beta = live ? beta_of(rb, p) : 0.f;
+    const float alpha = live ? expf(A * step_of(tile.rdt, bias, p)) : 1.f;
+    const float beta = live ? beta_of(tile.rb, p) : 0.f;
     const float beta_j = __shfl_sync(0xffffffffu, beta, j);
     float a[4], gj = 1.f, d = 1.f;
 #pragma unroll
@@ -195,19 +187,47 @@ __global__ void __launch_bounds__(WARPS * 32) delta_recurrent_kernel(const Delta
     }
   };
 
+  if (len == 0 && (warp < kStageWarps || !p.h_final)) return;
+  if (warp < kStageWarps) {
+    fetch(even, 0);
+    if (TT < len) fetch(odd, TT);
+    for (int t0 = 0; t0 < len; t0 += 2 * TT) {
+      stage(even, t0, 0);
+      __syncthreads();
+      if (t0 + 2 * TT < len) fetch(even, t0 + 2 * TT);
+      if (t0 + TT >= len) break;
+      stage(odd, t0 + TT, 1);
+      __syncthreads();
+      if (t0 + 3 * TT < len) fetch(odd, t0 + 3 * TT);
+    }
+    return;
+  }
+
+  const int r = (warp - kStageWarps) * (32 / LPR) + lane / LPR, s = lane % LPR;
+  const long long soff = (((long long)seq * p.H + h) * p.P + row0 + r) * kDState + 4 * s;
+  float2 S[E4][2];
+#pragma unroll
+  for (int j = 0; j < E4; ++j) {
+    const float4 x = p.h0 ? *reinterpret_cast<const float4 *>(p.h0 + soff + 4 * LPR * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+    S[j][0] = make_float2(x.x, x.y);
+    S[j][1] = make_float2(x.z, x.w);
+  }
+  const int yj = s & 3;  // lane s ends with S k_s (s < 4) or S q_{s - 4}, and the latter stores that token's y
   T *y = static_cast<T *>(p.y);
-  const long long yoff = base * p.ys + (long long)h * p.P + row0 + r;
-  if (len > 0) fetch(0);
+  long long yo = (base + yj) * p.ys + (long long)h * p.P + row0 + r;
   for (int t0 = 0, buf = 0; t0 < len; t0 += TT, buf ^= 1) {
-    stage(t0, buf);
     __syncthreads();
-    if (t0 + TT < len) fetch(t0 + TT);
     const int blocks = (min(TT, len - t0) + 3) / 4;
-#pragma unroll 1
+#pragma unroll 2
     for (int b = 0; b < blocks; ++b) {
       const Four &f = s_four[buf][b];
       const float *kp = &sk[buf][4 * b][4 * s], *qp = &sq[buf][4 * b][4 * s];
-      float2 kv[kHold ? 4 : 1][E4][2], acc[8];
+      const float4 g4 = *reinterpret_cast<const float4 *>(f.g), b4 = *reinterpret_cast<const float4 *>(f.beta);
+      const float4 v4 = *reinterpret_cast<const float4 *>(&sv[buf][r][4 * b]);
+      const float4 kk2 = *reinterpret_cast<const float4 *>(f.kk[2]), kk3 = *reinterpret_cast<const float4 *>(f.kk[3]);
+      const float4 end = *reinterpret_cast<const float4 *>(f.end);
+      const float kk1 = f.kk[1][0];
+      float2 kv[4][E4][2], acc[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] = make_float2(0.f, 0.f);
 #pragma unroll
@@ -221,10 +241,8 @@ __global__ void __launch_bounds__(WARPS * 32) delta_recurrent_kernel(const Delta
           acc[j] = __ffma2_rn(S[e][1], x1, acc[j]);
           acc[4 + j] = __ffma2_rn(S[e][0], make_float2(z.x, z.y), acc[4 + j]);
           acc[4 + j] = __ffma2_rn(S[e][1], make_float2(z.z, z.w), acc[4 + j]);
-          if (kHold) {
-            kv[kHold ? j : 0][e][0] = x0;
-            kv[kHold ? j : 0][e][1] = x1;
-          }
+          kv[j][e][0] = x0;
+          kv[j][e][1] = x1;
         }
       float x[8];  // S k_j, S q_j: their sums over the row's lanes, handed over like those of stage()
 #pragma unroll
@@ -238,33 +256,15 @@ __global__ void __launch_bounds__(WARPS * 32) delta_recurrent_kernel(const Delta
           x[j] = (up ? x[j + n] : x[j]) + __shfl_xor_sync(0xffffffffu, give, o);
         }
       }
-      constexpr int X = 8 / LPR;  // sums that a lane ends with: number X s ..
-      const float4 g4 = *reinterpret_cast<const float4 *>(f.g), b4 = *reinterpret_cast<const float4 *>(f.beta);
-      const float4 v4 = *reinterpret_cast<const float4 *>(&sv[buf][r][4 * b]);
       float dk[4], u[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) dk[j] = __shfl_sync(0xffffffffu, x[j % X], (lane & ~(LPR - 1)) | (j / X));
+      for (int j = 0; j < 4; ++j) dk[j] = __shfl_sync(0xffffffffu, x[0], (lane & ~(LPR - 1)) | j);
       u[0] = b4.x * fmaf(-g4.x, dk[0], v4.x);
-      u[1] = fmaf(-f.kk[1][0], u[0], b4.y * fmaf(-g4.y, dk[1], v4.y));
+      u[1] = fmaf(-kk1, u[0], b4.y * fmaf(-g4.y, dk[1], v4.y));
       u[2] = b4.z * fmaf(-g4.z, dk[2], v4.z);
       u[3] = b4.w * fmaf(-g4.w, dk[3], v4.w);
-      u[2] = fmaf(-f.kk[2][1], u[1], fmaf(-f.kk[2][0], u[0], u[2]));
-      u[3] = fmaf(-f.kk[3][2], u[2], fmaf(-f.kk[3][1], u[1], fmaf(-f.kk[3][0], u[0], u[3])));
-      if (s >= LPR / 2) {
-#pragma unroll
-        for (int c = 0; c < X; ++c) {
-          const int j = X * (s - LPR / 2) + c, t = t0 + 4 * b + j;
-          const float4 kq = *reinterpret_cast<const float4 *>(f.kq[j]);
-          // (what comes after token j is left out, not multiplied by zero: it may be NaN)
-          float o = fmaf(kq.x, u[0], f.g[j] * x[c]);
-          if (j >= 1) o = fmaf(kq.y, u[1], o);
-          if (j >= 2) o = fmaf(kq.z, u[2], o);
-          if (j >= 3) o = fmaf(kq.w, u[3], o);
-          const long long yo = (long long)t * p.ys + yoff;
-          if (t < len && in_bounds(yo, p.y_extent, p.err)) io<T>::st(y + yo, o);
-        }
-      }
-      const float4 end = *reinterpret_cast<const float4 *>(f.end);
+      u[2] = fmaf(-kk2.y, u[1], fmaf(-kk2.x, u[0], u[2]));
+      u[3] = fmaf(-kk3.z, u[2], fmaf(-kk3.y, u[1], fmaf(-kk3.x, u[0], u[3])));
       const float2 ge = make_float2(g4.w, g4.w);
       const float w[4] = {u[0] * end.x, u[1] * end.y, u[2] * end.z, u[3] * end.w};
 #pragma unroll
@@ -273,20 +273,17 @@ __global__ void __launch_bounds__(WARPS * 32) delta_recurrent_kernel(const Delta
         S[e][1] = __fmul2_rn(S[e][1], ge);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float2 x0, x1;
-          if (kHold) {
-            x0 = kv[kHold ? j : 0][e][0];
-            x1 = kv[kHold ? j : 0][e][1];
-          } else {
-            const float4 z = *reinterpret_cast<const float4 *>(kp + j * kDState + 4 * LPR * e);
-            x0 = make_float2(z.x, z.y);
-            x1 = make_float2(z.z, z.w);
-          }
           const float2 w2 = make_float2(w[j], w[j]);
-          S[e][0] = __ffma2_rn(w2, x0, S[e][0]);
-          S[e][1] = __ffma2_rn(w2, x1, S[e][1]);
+          S[e][0] = __ffma2_rn(w2, kv[j][e][0], S[e][0]);
+          S[e][1] = __ffma2_rn(w2, kv[j][e][1], S[e][1]);
         }
       }
+      const float4 kq = *reinterpret_cast<const float4 *>(f.kq[yj]);
+      // (what comes after token yj is left out, not multiplied by zero: it may be NaN)
+      const float o = fmaf(kq.w, yj >= 3 ? u[3] : 0.f, fmaf(kq.z, yj >= 2 ? u[2] : 0.f,
+                      fmaf(kq.y, yj >= 1 ? u[1] : 0.f, fmaf(kq.x, u[0], f.g[yj] * x[0]))));
+      if (s >= 4 && t0 + 4 * b + yj < len && in_bounds(yo, p.y_extent, p.err)) io<T>::st(y + yo, o);
+      yo += 4 * p.ys;
     }
   }
   if (p.h_final) {
@@ -390,11 +387,20 @@ __global__ void __launch_bounds__(WARPS * 32) delta_decode_kernel(const DeltaPla
 // 16 rows per CTA spread a small call over more SMs
 bool is_small(const DeltaPlan &p) { return (long long)p.B * p.H * p.P <= 64 * 2 * 148; }
 
+// The rows of a CTA: as few as leave one CTA per SM, since the rows of an SM share its shared-memory reads, and
+// as many as the registers allow once there are more.  Every choice gives the same bits.  256 tokens x H
+// heads of 64 rows, fp32, in us with CW = 2, 4, 8:  H = 8: 31, 38, 60;  32: 44, 40, 61;  64: 79, 75, 61;
+// 512: 527, 488, 392.
+template <typename T, int CW>
+cudaError_t launch_rows(const DeltaPlan &p, cudaStream_t s) {
+  delta_recurrent_kernel<T, CW><<<dim3(p.H * p.P / (4 * CW), p.B), (kStageWarps + CW) * 32, 0, s>>>(p);
+  return cudaGetLastError();
+}
 template <typename T>
 cudaError_t launch_recurrent(const DeltaPlan &p, cudaStream_t s) {
-  if (is_small(p)) delta_recurrent_kernel<T, 8, 4><<<dim3(p.H * p.P / 16, p.B), 128, 0, s>>>(p);
-  else delta_recurrent_kernel<T, 4, 8><<<dim3(p.H * p.P / 64, p.B), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  const long long rows = (long long)p.B * p.H * p.P;
+  if (rows <= 8 * 148) return launch_rows<T, 2>(p, s);
+  return rows <= 16 * 148 ? launch_rows<T, 4>(p, s) : launch_rows<T, 8>(p, s);
 }
 template <typename T>
 cudaError_t launch_decode(const DeltaPlan &p, cudaStream_t s) {
