@@ -80,13 +80,15 @@ bool packed(const ssd_delta_config_t *c, const int *cu, int nseq, Batch *b) {
   return true;
 }
 
-// The longest sequence from which AUTO takes the chunked kernel.
-constexpr int kChunkedFrom = 96;
-
+// The longest sequence from which AUTO takes the chunked kernels.  They cost two launches and a chunk's latency
+// (15 us); the recurrence costs its longest sequence, times its CTAs per SM once the state rows are more than
+// one CTA per SM holds.  Both in us, bf16, at 64, 96, 128 tokens: 8 heads of 64 rows 9.3 : 15.0, 12.4 : 16.5,
+// 15.6 : 16.6; at 16, 32, 64 tokens: 4 sequences of 32 heads 11.6 : 16.8, 18.4 : 16.9, 31.7 : 17.1.
 bool uses_chunks(const ssd_delta_config_t *c, const Batch &b) {
   if (b.rows == 0 || c->kernel == SSD_KERNEL_SIMT) return false;
   if (c->kernel == SSD_KERNEL_TENSOR) return true;
-  return c->io_dtype == SSD_BF16 && b.longest >= kChunkedFrom && tc_scan_available();
+  const bool one_each = (long long)b.nseq * c->nheads * c->headdim <= 16 * 148;
+  return c->io_dtype == SSD_BF16 && b.longest >= (one_each ? 128 : 28) && tc_scan_available();
 }
 
 struct Layout {
