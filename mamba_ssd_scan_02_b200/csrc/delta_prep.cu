@@ -327,7 +327,8 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
       const int r = r0 + 2 * i + (lane >> 4), c = lane & 15;
       const uint4 o = make_uint4(v[0], v[1], v[2], v[3]);
       *reinterpret_cast<uint4 *>(smem + OFF_K + r * kKPitch * 2 + 16 * c) = o;
-      if (blockIdx.z == 0) *reinterpret_cast<uint4 *>(tile + (c >> 3) * kHalf + swz(r, c & 7)) = o;
+      const int at = 32 * ((r & 63) >> 4) + 16 * kind + (r & 15);  // 16 K rows, the Q rows of the same tokens, ..
+      if (blockIdx.z == 0) *reinterpret_cast<uint4 *>(tile + (c >> 3) * kHalf + swz(at, c & 7)) = o;
     }
     // sums over 16 lanes; lane c of a half warp ends with row c / 2's
 #pragma unroll

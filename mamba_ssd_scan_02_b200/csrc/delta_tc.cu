@@ -68,7 +68,7 @@ constexpr uint32_t OFF_T = kDeep * kTile;
 constexpr uint32_t OFF_AT = OFF_T + 2 * kT;
 constexpr uint32_t OFF_VG = OFF_AT + 2 * kAT;
 constexpr uint32_t OFF_SB = OFF_VG + kDeep * kVG;  // S operands of the halves: [n][32 p hi, 32 p lo], 128 rows each
-constexpr uint32_t OFF_R = OFF_SB + 2 * kHalf;    // R operands of the halves: [token][32 p hi, 32 p lo], 64 rows each
+constexpr uint32_t OFF_R = OFF_SB + 2 * kHalf;    // R operands: [token][32 p of each half], 64 rows of hi, 64 of lo
 constexpr uint32_t OFF_MAXS = OFF_R + 2 * 8192;      // largest |S| per chain warp, two chunks
 constexpr uint32_t OFF_MAXV = OFF_MAXS + 64;      // bound of what the chunk adds, per place in the ring
 constexpr uint32_t OFF_BAR = OFF_MAXV + 64;
@@ -83,12 +83,12 @@ enum {
   BAR_AT = BAR_T + 2,              // [2] A T loaded
   BAR_M = BAR_AT + 2,              // [2] M done
   BAR_MREADY = BAR_M + 2,          // [2] M operand in tensor memory (4 warps)
-  BAR_SREADY = BAR_MREADY + 2,     // [2 halves] S operand written (4 warps)
-  BAR_RREADY = BAR_SREADY + 2,     // [2 halves] R operand written, D1 read (4 warps)
-  BAR_D1 = BAR_RREADY + 2,         // [2 halves] K S^T, Q S^T done
-  BAR_S = BAR_D1 + 2,              // [2 halves] M R done
-  BAR_O = BAR_S + 2,               // [2 halves] A T R done
-  BAR_DONE = BAR_O + 2,            // [2] nothing of an issuer's left in flight
+  BAR_SREADY = BAR_MREADY + 2,     // S operand written (8 warps)
+  BAR_RREADY = BAR_SREADY + 1,     // [2 halves] R operand written, D1 read (4 warps)
+  BAR_D1 = BAR_RREADY + 2,         // K S^T, Q S^T done
+  BAR_S = BAR_D1 + 1,              // [2 halves] M R done
+  BAR_O = BAR_S + 2,               // A T R done
+  BAR_DONE = BAR_O + 1,            // [2] nothing of an issuer's left in flight
   kNumBars = BAR_DONE + 2
 };
 constexpr uint32_t OFF_MISC = OFF_BAR + 8 * 32;   // [0] TMEM base, [1] abort flag, [2] the same for the last waits
@@ -96,15 +96,19 @@ constexpr uint32_t kSmem = OFF_MISC + 16 + 1024;  // room to align the base to 1
 static_assert(kNumBars <= 32 && kSmem <= 232448, "shared memory");
 static_assert(OFF_SB % 1024 == 0 && OFF_R % 1024 == 0 && OFF_T % 1024 == 0 && OFF_VG % 1024 == 0, "swizzle alignment");
 
-// TMEM columns.  K rows are lanes 0-63 of D1, Q rows lanes 64-127, as are the rows of A T R (lanes 0-63
-// of it are never used).  D1 and S have per half 32 columns of the products with hi, 32 of those with
-// lo, O 32 columns.  The M operand replaces M: tokens 32 b .. 32 b + 31 lie in the columns 32 b .. of their own 32 fp32
-// columns, hi first, lo 16 columns on.
-constexpr uint32_t TM_M = 0, TM_D1 = 128, TM_S = 256, TM_O = 384, TM_COLS = 512;
+// TMEM columns.  M: twice 64 columns of the product with T's hi and 64 of that with its lo; the M operand
+// replaces the former (tokens 32 b .. 32 b + 31 in the columns 32 b .. , hi first, lo 16 columns on).  Of every 32
+// lanes of D1 the first 16 are K rows, the others the Q rows of the same tokens, as are the rows of A T R (the other
+// lanes of it are never used): each of the four warps that can read a quarter of the lanes then has as much to
+// convert (with the K rows in lanes 0-63, two of them had all of R to convert, on two of the four schedulers; 240
+// us where this takes 232, 8192 tokens x 128 heads).  D1 has
+// per half 32 columns of the products with hi, 32 of those with lo, S and O 32 columns.
+constexpr uint32_t TM_M = 0, TM_D1 = 256, TM_S = 384, TM_O = 448, TM_COLS = 512;
 
-constexpr uint32_t IDESC_N64 = idesc_f16(128, 64, false, true, kFmtF16);   // [K; Q] . S, M (TMEM) . R
-constexpr uint32_t IDESC_N32 = idesc_f16(128, 32, false, true, kFmtF16);   // M_lo (TMEM) . R_hi, A T . R_hi
-constexpr uint32_t IDESC_M = idesc_f16(128, 64, true, false, kFmtF16);     // K^T . T
+constexpr uint32_t IDESC_D1 = idesc_f16(128, 128, false, true, kFmtF16);  // [K; Q] . S of both halves
+constexpr uint32_t IDESC_M = idesc_f16(128, 128, true, false, kFmtF16);   // K^T . [T_hi, T_lo]
+constexpr uint32_t IDESC_S = idesc_f16(128, 32, false, true, kFmtF16);    // M (TMEM) . R of a half
+constexpr uint32_t IDESC_O = idesc_f16(128, 64, false, true, kFmtF16);    // A T . R_hi of both halves
 
 // A bounded wait.  A try suspends the warp for a while in hardware; after every 256 the abort flag is
 // looked at, and after 2^17 times that (about a second) the flag is set to 2.  In one piece of
@@ -192,31 +196,51 @@ __device__ __forceinline__ void commit(uint32_t bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
+// The operands that the halves share are read once for both: an SS product takes its operands' bytes / 128
+// clocks (N = 64: 49, N = 128: 65), a TS product its multiply-adds.
 __device__ __forceinline__ void issue_D1(uint32_t kq, uint32_t sbuf, uint32_t d) {
-  const uint32_t a = op_lo(kq, 16), b = op_lo(sbuf, 8192);
+  const uint32_t a = op_lo(kq, 16), b = op_lo(sbuf, kHalf);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) mma_ss<IDESC_N64>(d, a + kstep(j), b + j * 128, j > 0);
+  for (int j = 0; j < 8; ++j) mma_ss<IDESC_D1>(d, a + kstep(j), b + j * 128, j > 0);
 }
 __device__ __forceinline__ void issue_M(uint32_t kq, uint32_t t, uint32_t d) {
   const uint32_t a = op_lo(kq, kHalf), b = op_lo(t, 16);
 #pragma unroll
-  for (int j = 0; j < 8; ++j)  // hi, then lo
-    mma_ss<IDESC_M>(d, a + (j & 3) * 128, b + (j >> 2) * 512 + (j & 3) * 2, j > 0);
+  for (int j = 0; j < 4; ++j) mma_ss<IDESC_M>(d, a + j * 256, b + j * 2, j > 0);  // 16 K rows of every 32
 }
-// d = M_hi R_hi + M_lo R_hi | M_hi R_lo  (64 tokens)
-__device__ __forceinline__ void issue_S(uint32_t m, uint32_t r, uint32_t d) {
-  const uint32_t b = op_lo(r, 8192);
+// d = M_lo R_hi + M_hi R_lo + M_hi R_hi  (64 tokens; the small ones first).  The half's columns of R begin
+// 64 half bytes into its rows.
+__device__ __forceinline__ void issue_S(uint32_t m, uint32_t r, int half, uint32_t d) {
+  const uint32_t hi = op_lo(r, 8192) + 4 * half, lo = op_lo(r + 8192, 8192) + 4 * half;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) mma_ts<IDESC_N64>(d, m + tstep(j), b + 128 * j, j > 0);
+  for (int j = 0; j < 4; ++j) {
+    mma_ts<IDESC_S>(d, m + tstep(j) + 16, hi + 128 * j, j > 0);
+    mma_ts<IDESC_S>(d, m + tstep(j), lo + 128 * j, true);
+  }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) mma_ts<IDESC_N32>(d, m + tstep(j) + 16, b + 128 * j, true);
+  for (int j = 0; j < 4; ++j) mma_ts<IDESC_S>(d, m + tstep(j), hi + 128 * j, true);
 }
-// A T . R_hi: rows 64-127 of the A operand are A T's; rows 0-63 are what lies 8 KB before it, and their
-// results are not used
+// A T . R_hi.  The rows of A T are the second 16 of every 32 rows of the A operand; the first 16 are the other
+// chunk's (or, before the first place, the end of T), and their results are not used.
 __device__ __forceinline__ void issue_O(uint32_t at, uint32_t r, uint32_t d) {
-  const uint32_t a = op_lo(at - 8192, 16), b = op_lo(r, 8192);
+  const uint32_t a = op_lo(at - 2048, 16), b = op_lo(r, 8192);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) mma_ss<IDESC_N32>(d, a + 2 * j, b + 128 * j, j > 0);
+  for (int j = 0; j < 4; ++j) mma_ss<IDESC_O>(d, a + 2 * j, b + 128 * j, j > 0);
+}
+
+// 16 TMEM lanes (from taddr's on) x 32 columns: thread l has of rows l / 4 and l / 4 + 8 the columns 8 b + 2 (l % 4) and
+// the next, at 4 b and 4 b + 2.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // Powers of two that bring a quantity bounded by m to [64, 128) and back.  Headroom: with alpha <= 1
@@ -251,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(BAR(i), i >= BAR_MREADY && i < BAR_D1 ? 4 : 1);
+      mbar_init(BAR(i), i == BAR_SREADY ? 8 : i >= BAR_MREADY && i < BAR_D1 ? 4 : 1);
     misc[1] = misc[2] = 0;
     fence_mbar_init();
   }
@@ -268,33 +292,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const bool lead = lane == 0;
   if (warp == 12) {
-    // ------------------------------------------------------------------ MMAs of the chains, one half's after the
-    // other's: while those of one run, the other converts
+    // ------------------------------------------------------------------ MMAs of the chains
     Ring<kDeep> r;
     bool ok = true;
     for (int c = 0; c < nck && ok; ++c, r.next()) {
       ok = wait(BAR_READY + r.at, r.parity);
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        ok = wait(BAR_SREADY + half, c & 1) && ok;
-        tc_fence_after();
-        issue_D1(sb + r.at * kTile, sb + OFF_SB + half * kHalf, tmem + TM_D1 + 64 * half);
-        commit(BAR(BAR_D1 + half));
-      }
+      ok = wait(BAR_SREADY, c & 1) && ok;
+      tc_fence_after();
+      issue_D1(sb + r.at * kTile, sb + OFF_SB, tmem + TM_D1);
+      commit(BAR(BAR_D1));
       ok = wait2(BAR_MREADY, c) && ok;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         ok = wait(BAR_RREADY + half, c & 1) && ok;
         tc_fence_after();
-        issue_S(tmem + TM_M + 64 * (c & 1), sb + OFF_R + half * 8192, tmem + TM_S + 64 * half);
+        issue_S(tmem + TM_M + 128 * (c & 1), sb + OFF_R, half, tmem + TM_S + 32 * half);
         commit(BAR(BAR_S + half));
       }
       ok = wait2(BAR_AT, c) && ok;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        issue_O(sb + OFF_AT + (c & 1) * kAT, sb + OFF_R + half * 8192, tmem + TM_O + 32 * half);
-        commit(BAR(BAR_O + half));
-      }
+      issue_O(sb + OFF_AT + (c & 1) * 2048, sb + OFF_R, tmem + TM_O);
+      commit(BAR(BAR_O));
       commit(BAR(BAR_EMPTY + r.at));
       ok = __all_sync(0xffffffffu, ok);
     }
@@ -313,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      issue_M(sb + r.at * kTile, sb + OFF_T + (c & 1) * kT, tmem + TM_M + 64 * (c & 1));
+      issue_M(sb + r.at * kTile, sb + OFF_T + (c & 1) * kT, tmem + TM_M + 128 * (c & 1));
       commit(BAR(BAR_M + (c & 1)));
     }
     commit(BAR(BAR_DONE + 1));
@@ -352,7 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c != 1 && n_at < nck) {
           const uint32_t at = BAR(BAR_AT + (n_at & 1));
           mbar_arrive_expect_tx(at, kAT);
-          bulk_load(sb + OFF_AT + (n_at & 1) * kAT, rec + n_at * rec_step, kAT, at);
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i)  // the two places alternate by 16 rows
+            bulk_load(sb + OFF_AT + (n_at & 1) * 2048 + i * 4096, rec + n_at * rec_step + i * 2048, 2048, at);
           ++n_at;
         }
       }
@@ -423,16 +442,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float4 *f = reinterpret_cast<const float4 *>(smem + OFF_VG + r.at * kVG + OFF_END);
 #pragma unroll 1
       for (int b = 0; b < 2; ++b) {
-        const uint32_t at = tmem + TM_M + 64 * (c & 1) + 32 * b + lane_off;
-        float m[32];
+        const uint32_t at = tmem + TM_M + 128 * (c & 1) + 32 * b + lane_off;
+        float m[32], e[32];
         uint32_t hv[16], lv[16];
         tmem_ld32(at, m);
+        tmem_ld32(at + 64, e);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float4 x = f[8 * b + j];
-          split2(__fmul2_rn(make_float2(m[4 * j], m[4 * j + 1]), make_float2(x.x, x.y)), hv[2 * j], lv[2 * j]);
-          split2(__fmul2_rn(make_float2(m[4 * j + 2], m[4 * j + 3]), make_float2(x.z, x.w)), hv[2 * j + 1], lv[2 * j + 1]);
+          const auto sum = [&](int i) { return __fadd2_rn(make_float2(m[i], m[i + 1]), make_float2(e[i], e[i + 1])); };
+          split2(__fmul2_rn(sum(4 * j), make_float2(x.x, x.y)), hv[2 * j], lv[2 * j]);
+          split2(__fmul2_rn(sum(4 * j + 2), make_float2(x.z, x.w)), hv[2 * j + 1], lv[2 * j + 1]);
         }
         tmem_st16(at, hv);
         tmem_st16(at + 16, lv);
@@ -445,12 +466,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------------ the chains
     const int hf = warp >> 2;                // half: state rows (columns of S and O) 32 hf ..
-    const bool is_q = q4 >= 2;
-    const int row = 32 * (q4 & 1) + lane;    // token of this thread's lane of D1 and O
+    const int row = 16 * q4 + (lane >> 2);   // this thread's tokens of D1 and O: row, row + 8
+    const int col = 2 * (lane & 3);          // its columns of them: 8 b + col, 8 b + col + 1, b = 0 .. 3
     const int n = 32 * q4 + lane;            // state column of this thread
     const long long soff = (((long long)seq * p.H + h) * p.P + 64 * ph + 32 * hf) * kDState + n;
     uint32_t *max_s = reinterpret_cast<uint32_t *>(smem + OFF_MAXS) + 8 * hf;
-    const uint32_t t_d1 = tmem + TM_D1 + 64 * hf, t_s = tmem + TM_S + 64 * hf, t_o = tmem + TM_O + 32 * hf;
+    const uint32_t t_d1 = tmem + TM_D1 + 64 * hf, t_s = tmem + TM_S + 32 * hf, t_o = tmem + TM_O + 32 * hf;
     float2 S[16];  // the state, times sc.x
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -474,56 +495,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     float2 sc = state_scale(m);
 #pragma unroll
     for (int i = 0; i < 16; ++i) S[i] = __fmul2_rn(S[i], make_float2(sc.x, sc.x));
-    // K rows: the chunk's V; Q rows: 2^cs Q S^T of the chunk whose y is still to come
-    float2 hold[16];
-    float gamma = 0.f, gamma_end = 0.f, beta = 0.f, rho = 0.f, vmax = 0.f;  // of the chunk
-    float back_o = 0.f, rho_y = 0.f;                                         // of the y to come
+    uint32_t v[2][4];                  // the chunk's V, pairs
+    float2 hold[2][4];                 // 2^cs Q S^T of the chunk whose y is still to come
+    float gamma[2], beta[2], rho_k[2], rho_q[2], gamma_end = 0.f, vmax = 0.f;  // of the chunk
+    float back_o = 0.f, rho_y[2];      // of the y to come
     Ring<kDeep> ring;  // of the rows to load next
     const auto load_rows = [&](int c) {
       const unsigned char *stage = smem + OFF_VG + ring.at * kVG;
       const auto arr = [&](uint32_t off) { return reinterpret_cast<const float *>(stage + off); };
+      const auto rho = [&](uint32_t off) { return reinterpret_cast<const float *>(smem + ring.at * kTile + off); };
       const bool ok = wait(BAR_READY + ring.at, ring.parity);
       vmax = reinterpret_cast<const float *>(smem + OFF_MAXV)[ring.at];
-      gamma = arr(OFF_GAMMA)[row];
       gamma_end = arr(OFF_GAMMA)[C - 1];
-      rho = reinterpret_cast<const float *>(smem + ring.at * kTile + (is_q ? OFF_RHOQ : OFF_RHOK))[row];
-      if (!is_q) {
-        const bool live = c * C + row < len;  // (the rows after may hold anything)
-        beta = live ? arr(OFF_BETA)[row] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 u = live ? *reinterpret_cast<const uint4 *>(stage + swz(row, 4 * hf + i)) : make_uint4(0, 0, 0, 0);
-          hold[2 * i] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
-          hold[2 * i + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+      for (int i = 0; i < 2; ++i) {
+        const int t = row + 8 * i;
+        const bool live = c * C + t < len;  // (the rows after may hold anything)
+        gamma[i] = arr(OFF_GAMMA)[t];
+        beta[i] = live ? arr(OFF_BETA)[t] : 0.f;
+        rho_k[i] = rho(OFF_RHOK)[t];
+        rho_q[i] = rho(OFF_RHOQ)[t];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t u = *reinterpret_cast<const uint32_t *>(stage + swz(t, 4 * hf + b) + 2 * col);
+          v[i][b] = live ? u : 0u;
         }
       }
       ring.next();
       return ok;
     };
-    const auto put_y = [&](int c) {  // Q rows: y of chunk c
-      wait(BAR_O + hf, c & 1);
+    const auto put_y = [&](int c) {  // y of chunk c
+      wait(BAR_O, c & 1);
       __syncwarp();
       tc_fence_after();
-      const int t = c * C + row;
-      const long long yo = (base + t) * p.ys + (long long)h * p.P + 64 * ph + 32 * hf;
-      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.y) + yo);
-      const bool store = t < len && in_bounds(yo + 31, p.y_extent, p.err);
-      const float2 b2 = make_float2(back_o, back_o), r2 = make_float2(rho_y, rho_y);
+      float o[16];
+      tmem_ld_rows(t_o + lane_off + (16u << 16), o);
+      tmem_ld_wait();
+      const float2 b2 = make_float2(back_o, back_o);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float o[16];
-        tmem_ld16(t_o + 16 * x + lane_off, o);
-        tmem_ld_wait();
-        uint32_t u[8];
+      for (int i = 0; i < 2; ++i) {
+        const int t = c * C + row + 8 * i;
+        const long long yo = (base + t) * p.ys + (long long)h * p.P + 64 * ph + 32 * hf + col;
+        const bool store = t < len && in_bounds(yo + 25, p.y_extent, p.err);
+        const float2 r2 = make_float2(rho_y[i], rho_y[i]);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.y) + yo);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 f = __fmul2_rn(r2, __ffma2_rn(b2, make_float2(o[2 * i], o[2 * i + 1]), hold[8 * x + i]));
-          const __nv_bfloat162 v = __float22bfloat162_rn(f);
-          u[i] = *reinterpret_cast<const uint32_t *>(&v);
-        }
-        if (store) {
-          dst[2 * x] = make_uint4(u[0], u[1], u[2], u[3]);
-          dst[2 * x + 1] = make_uint4(u[4], u[5], u[6], u[7]);
+        for (int b = 0; b < 4; ++b) {
+          const float2 f = __fmul2_rn(r2, __ffma2_rn(b2, make_float2(o[4 * b + 2 * i], o[4 * b + 2 * i + 1]), hold[i][b]));
+          const __nv_bfloat162 x = __float22bfloat162_rn(f);
+          if (store) dst[4 * b] = *reinterpret_cast<const uint32_t *>(&x);
         }
       }
     };
@@ -542,43 +562,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async();
       tc_fence_before();
       __syncwarp();
-      if (lead) mbar_arrive(BAR(BAR_SREADY + hf));
+      if (lead) mbar_arrive(BAR(BAR_SREADY));
       // while K S^T runs: y of the chunk before, the bound of |S|
-      if (is_q && c > 0) put_y(c - 1);
+      if (c > 0) put_y(c - 1);
       publish_max(c & 1);
       const float2 rsc = state_scale(fmaxf(m, vmax));
-      rho_y = rho;
       back_o = rsc.y;
-      const float g = gamma * sc.y, gk = -g * rho, b = beta * rsc.x;
-      const float2 g2 = make_float2(g, g), k2 = make_float2(gk, gk), b2 = make_float2(b, b);
-      ok = wait(BAR_D1 + hf, c & 1) && ok;
+      ok = wait(BAR_D1, c & 1) && ok;
       __syncwarp();
       tc_fence_after();
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      {
         float d[16], e[16];
-        tmem_ld16(t_d1 + 16 * x + lane_off, d);
-        tmem_ld16(t_d1 + 32 + 16 * x + lane_off, e);
+        tmem_ld_rows(t_d1 + lane_off, d);
+        tmem_ld_rows(t_d1 + 32 + lane_off, e);
         tmem_ld_wait();
-        if (is_q) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            hold[8 * x + i] = __fmul2_rn(g2, __fadd2_rn(make_float2(d[2 * i], d[2 * i + 1]), make_float2(e[2 * i], e[2 * i + 1])));
-        } else {
-          uint32_t hv[8], lv[8];
+        for (int i = 0; i < 2; ++i) {
+          const float g = -gamma[i] * sc.y * rho_k[i], bt = beta[i] * rsc.x;
+          const float2 k2 = make_float2(g, g), b2 = make_float2(bt, bt);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 vp = hold[4 * x + i / 2];  // two bf16 pairs
-            const uint32_t u = __float_as_uint(i & 1 ? vp.y : vp.x);
-            const float2 v = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-            const float2 ks = __fadd2_rn(make_float2(d[2 * i], d[2 * i + 1]), make_float2(e[2 * i], e[2 * i + 1]));
-            split2(__fmul2_rn(b2, __ffma2_rn(k2, ks, v)), hv[i], lv[i]);
+          for (int b = 0; b < 4; ++b) {
+            const int x = 4 * b + 2 * i;
+            const float2 vp = make_float2(__uint_as_float(v[i][b] << 16), __uint_as_float(v[i][b] & 0xffff0000u));
+            const float2 ks = __fadd2_rn(make_float2(d[x], d[x + 1]), make_float2(e[x], e[x + 1]));
+            uint32_t hv, lv;
+            split2(__fmul2_rn(b2, __ffma2_rn(k2, ks, vp)), hv, lv);
+            unsigned char *o = smem + OFF_R + swz(row + 8 * i, 4 * hf + b) + 2 * col;
+            *reinterpret_cast<uint32_t *>(o) = hv;
+            *reinterpret_cast<uint32_t *>(o + 8192) = lv;
           }
-          unsigned char *o = smem + OFF_R + hf * 8192;
+        }
+        tmem_ld_rows(t_d1 + lane_off + (16u << 16), d);
+        tmem_ld_rows(t_d1 + 32 + lane_off + (16u << 16), e);
+        tmem_ld_wait();
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            *reinterpret_cast<uint4 *>(o + swz(row, 2 * x + u)) = make_uint4(hv[4 * u], hv[4 * u + 1], hv[4 * u + 2], hv[4 * u + 3]);
-            *reinterpret_cast<uint4 *>(o + swz(row, 4 + 2 * x + u)) = make_uint4(lv[4 * u], lv[4 * u + 1], lv[4 * u + 2], lv[4 * u + 3]);
+        for (int i = 0; i < 2; ++i) {
+          const float g = gamma[i] * sc.y;
+          rho_y[i] = rho_q[i];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int x = 4 * b + 2 * i;
+            hold[i][b] = __fmul2_rn(make_float2(g, g), __fadd2_rn(make_float2(d[x], d[x + 1]), make_float2(e[x], e[x + 1])));
           }
         }
       }
@@ -601,17 +625,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 16; ++i) S[i] = __fmul2_rn(S[i], ge2);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float d[16], e[16];
+        float d[16];
         tmem_ld16(t_s + 16 * x + lane_off, d);
-        tmem_ld16(t_s + 32 + 16 * x + lane_off, e);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          S[8 * x + i] = __ffma2_rn(y2, __fadd2_rn(make_float2(d[2 * i], d[2 * i + 1]), make_float2(e[2 * i], e[2 * i + 1])), S[8 * x + i]);
+        for (int i = 0; i < 8; ++i) S[8 * x + i] = __ffma2_rn(y2, make_float2(d[2 * i], d[2 * i + 1]), S[8 * x + i]);
       }
     }
     if (ok) {
-      if (is_q && nck > 0) put_y(nck - 1);
+      if (nck > 0) put_y(nck - 1);
       if (p.h_final) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
