@@ -58,18 +58,16 @@ __global__ void __launch_bounds__(kThreads) state_store_kernel(const StateCacheP
   long long state, cache;
   if (!entry(p, true, blockIdx.y, &state, &cache)) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const long long at0 = (long long)blockIdx.x * kPerCta + warp * kRow;
+  const long long at0 = (long long)blockIdx.x * kPerCta + warp * kUnroll * kRow;
   const float *src = p.states + state * p.elems + 4 * lane;
   float4 x[kUnroll];
 #pragma unroll
-  for (int i = 0; i < kUnroll; ++i) {
-    const long long at = at0 + (long long)i * (kThreads / 32) * kRow;
-    if (at < p.elems) x[i] = __ldcs(reinterpret_cast<const float4 *>(src + at));
-  }
+  for (int i = 0; i < kUnroll; ++i)  // (steps past the end read the last one: no branch between the loads)
+    x[i] = __ldcs(reinterpret_cast<const float4 *>(src + min(at0 + i * kRow, p.elems - kRow)));
+  uint32_t scales = 0;  // lane i: the four scale bytes of step i
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
-    const long long at = at0 + (long long)i * (kThreads / 32) * kRow;
-    if (at >= p.elems) break;
+    const long long at = at0 + i * kRow;
     // the largest magnitude as an integer: a NaN ranks above infinity, which ranks above the rest
     const uint32_t a = __float_as_uint(x[i].x) & 0x7fffffffu, b = __float_as_uint(x[i].y) & 0x7fffffffu;
     const uint32_t c = __float_as_uint(x[i].z) & 0x7fffffffu, d = __float_as_uint(x[i].w) & 0x7fffffffu;
@@ -93,11 +91,14 @@ __global__ void __launch_bounds__(kThreads) state_store_kernel(const StateCacheP
     uint32_t word = byte << (lane & 24);
     word |= __shfl_xor_sync(0xffffffffu, word, 8);
     word |= __shfl_xor_sync(0xffffffffu, word, 16);
+    if (lane == i) scales = word;
     const long long out = cache * p.elems + at;
-    if (!in_bounds(out + kRow - 1, p.cache_extent, p.err)) continue;
-    *reinterpret_cast<uint32_t *>(p.cache + out + 4 * lane) = bits;
-    if (lane == 0) *reinterpret_cast<uint32_t *>(p.scales + out / 32) = word;
+    if (at < p.elems && in_bounds(out + kRow - 1, p.cache_extent, p.err))
+      *reinterpret_cast<uint32_t *>(p.cache + out + 4 * lane) = bits;
   }
+  const long long at = at0 + lane * kRow, out = cache * p.elems + at;
+  if (lane < kUnroll && at < p.elems && in_bounds(out + kRow - 1, p.cache_extent, p.err))
+    *reinterpret_cast<uint32_t *>(p.scales + out / 32) = scales;
 }
 
 template <bool kE4m3>
@@ -105,19 +106,17 @@ __global__ void __launch_bounds__(kThreads) state_load_kernel(const StateCachePl
   long long state, cache;
   if (!entry(p, false, blockIdx.y, &state, &cache)) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const long long at0 = (long long)blockIdx.x * kPerCta + warp * kRow;
+  const long long at0 = (long long)blockIdx.x * kPerCta + warp * kUnroll * kRow;
   uint32_t x[kUnroll], sc[kUnroll];
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
-    const long long at = at0 + (long long)i * (kThreads / 32) * kRow, in = cache * p.elems + at;
-    if (at < p.elems) {
-      x[i] = __ldcs(reinterpret_cast<const uint32_t *>(p.cache + in + 4 * lane));
-      sc[i] = *(p.scales + in / 32 + lane / 8);
-    }
+    const long long in = cache * p.elems + min(at0 + i * kRow, p.elems - kRow);
+    x[i] = __ldcs(reinterpret_cast<const uint32_t *>(p.cache + in + 4 * lane));
+    sc[i] = *(p.scales + in / 32 + lane / 8);
   }
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
-    const long long at = at0 + (long long)i * (kThreads / 32) * kRow;
+    const long long at = at0 + i * kRow;
     if (at >= p.elems) break;
     // 2^e: byte 0 is the subnormal 2^-127; 255 is NaN
     const float f = __uint_as_float(sc[i] == 255 ? 0x7fffffffu : sc[i] == 0 ? 0x400000u : sc[i] << 23);

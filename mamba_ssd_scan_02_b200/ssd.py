@@ -507,13 +507,13 @@ def _rows(t, name, dtype, device, shape):
     evenly spaced: [B, L, width] rows are L * stride apart between batch rows."""
     _check_arg(t, name, dtype, device, shape)
     st = t.stride()
-    if len(shape) == 2 and st[1] == 1:
-        # at most one row: any stride that holds it and keeps the alignment rule
-        return t.data_ptr(), st[0] if shape[0] > 1 else (shape[1] + 7) // 8 * 8
+    if st[-1] == 1 and shape[-2] > 1 and (len(shape) == 2 or st[0] == shape[1] * st[1] or shape[0] == 1):
+        return t.data_ptr(), st[-2]  # (most calls)
     many = [i for i in range(len(shape) - 1) if shape[i] != 1]
     if st[-1] != 1 and shape[-1] > 1 and 0 not in shape:
         raise ValueError(f"{name}: channels must be contiguous")
     if not many or 0 in shape:
+        # at most one row: any stride that holds it and keeps the alignment rule
         return t.data_ptr(), (shape[-1] + 7) // 8 * 8
     if len(many) == 2 and st[0] != shape[1] * st[1]:
         raise ValueError(f"{name}: batch rows must be seqlen * row_stride apart")
