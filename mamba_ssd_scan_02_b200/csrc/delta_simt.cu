@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(WARPS * 32) delta_decode_kernel(const DeltaPla
   constexpr int R = WARPS * 32 / LPR;   // state rows of this CTA
   constexpr int E4 = kDState / LPR / 4; // float4s of a row per lane
   constexpr int NT = WARPS * 32;
+  constexpr bool kStream = LPR == 4;    // a large batch
   __shared__ __align__(16) float sq[kDState], sk[kDState];
   __shared__ float s_kq;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -379,8 +380,13 @@ __global__ void __launch_bounds__(WARPS * 32) delta_decode_kernel(const DeltaPla
   for (int j = 0; j < E4; ++j) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) S[j][e] = fmaf(u, kv[j][e], alpha * S[j][e]);
-    if (in_bounds(soff + 4 * LPR * j + 3, p.state_extent, p.err))
-      *reinterpret_cast<float4 *>(p.h_final + soff + 4 * LPR * j) = make_float4(S[j][0], S[j][1], S[j][2], S[j][3]);
+    if (!in_bounds(soff + 4 * LPR * j + 3, p.state_extent, p.err)) continue;
+    float4 *dst = reinterpret_cast<float4 *>(p.h_final + soff + 4 * LPR * j);
+    const float4 x = make_float4(S[j][0], S[j][1], S[j][2], S[j][3]);
+    // states beyond the L2 cache leave it first: 64 states of 128 heads 94.5 -> 90.3 us.  A small batch's stay, for
+    // its next step.
+    if (kStream) __stcs(dst, x);
+    else *dst = x;
   }
 }
 
