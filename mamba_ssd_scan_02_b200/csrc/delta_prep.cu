@@ -205,6 +205,10 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+// four 8 x 8 matrices from fragments like those of an accumulator; lane i gives the address of row i % 8 of number i / 8
+__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -472,22 +476,26 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
     // T operands: 8 elements of a row per lane, of the blocks on and above the diagonal; hi also over the
     // row in w, for A T
 #pragma unroll
-    for (int rb = 0; rb < 4; ++rb) {
+    for (int half = 0; half < 2; ++half) {  // two blocks of 16 rows at a time: all reads first
       constexpr uint4 zero = {0, 0, 0, 0};
-      const int units = 8 - 2 * rb;
-float *row[4];
-      float4 a[4], b[4];
+      float *row[7];
+      float4 a[7], b[7];
 #pragma unroll
-      for (int k = 0; k < 4 - rb; ++k) {
-        const int x = 32 * k + lane;
+      for (int k = 0; k < 7 - 4 * half; ++k) {
+        const int rb = 2 * half + (k >= 4 - 2 * half), units = 8 - 2 * rb, x = 32 * (k >= 4 - 2 * half ? k - 4 + 2 * half : k) + lane;
         row[k] = w + row_start(16 * rb) + (x / units) * pitch(16 * rb) + 4 * (x % units);
-        a[k] = *reinterpret_cast<const float4 *>(row[k] + 4 * (x % units));
-        b[k] = *reinterpret_cast<const float4 *>(row[k] + 4 * (x % units) + 4);
+        // (the second four lanes of a row read their halves in the other order: else they meet the first's banks)
+        const float *src = row[k] + 4 * (x % units);
+        const int odd = (x % units) & 4;
+        const float4 f = *reinterpret_cast<const float4 *>(src + odd), g = *reinterpret_cast<const float4 *>(src + 4 - odd);
+        a[k] = odd ? g : f;
+        b[k] = odd ? f : g;
       }
       __syncwarp();
 #pragma unroll
-      for (int k = 0; k < 4 - rb; ++k) {
-        const int x = 32 * k + lane, j = 16 * rb + x / units, u = 2 * rb + x % units;
+      for (int k = 0; k < 7 - 4 * half; ++k) {
+        const int rb = 2 * half + (k >= 4 - 2 * half), units = 8 - 2 * rb, x = 32 * (k >= 4 - 2 * half ? k - 4 + 2 * half : k) + lane;
+        const int j = 16 * rb + x / units, u = 2 * rb + x % units;
         uint4 hv, lv;
         split2(make_float2(a[k].x, a[k].y), hv.x, lv.x);
         split2(make_float2(a[k].z, a[k].w), hv.y, lv.y);
@@ -498,11 +506,13 @@ float *row[4];
         *reinterpret_cast<uint4 *>(rec + 8192 + swz(j, u)) = lv;
       }
 #pragma unroll
-      for (int x = lane; x < 32 * rb; x += 32) {
-        const int j = 16 * rb + (x & 15), u = x >> 4;
-        *reinterpret_cast<uint4 *>(rec + swz(j, u)) = zero;
-        *reinterpret_cast<uint4 *>(rec + 8192 + swz(j, u)) = zero;
-      }
+      for (int rb = 2 * half; rb < 2 * half + 2; ++rb)
+#pragma unroll
+        for (int x = lane; x < 32 * rb; x += 32) {
+          const int j = 16 * rb + (x & 15), u = x >> 4;
+          *reinterpret_cast<uint4 *>(rec + swz(j, u)) = zero;
+          *reinterpret_cast<uint4 *>(rec + 8192 + swz(j, u)) = zero;
+        }
     }
     __syncwarp();
     // A T: tiles on and below the diagonal.  Decays to a token of an earlier 16 in two factors, both at most
@@ -514,7 +524,9 @@ float *row[4];
 #pragma unroll
       for (int kk = rb; kk < 4; ++kk)
         ldmatrix4(b[rb][kk], tt + 4 * row_start(16 * rb) + ((lane & 7) + (lane >> 4) * 8) * 4 * pitch(16 * rb) + 32 * (kk - rb));
-    unsigned char *out = rec + 2 * 8192 + 4 * (lane & 3);
+    __syncwarp();  // w is free for the image of A T
+    unsigned char *image = reinterpret_cast<unsigned char *>(w);
+    const uint32_t im = tc::smem_u32(w);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
       uint32_t a[4][4];
@@ -523,37 +535,45 @@ float *row[4];
       const int t = 16 * mt + (lane >> 2);
       const float d0 = s_rel[t], d1 = s_rel[t + 8], rt0 = ex2(d0), rt1 = ex2(d1);
 #pragma unroll
-      for (int nt = 0; nt < 2 * mt + 2; ++nt) {
-        float c[4] = {};
+      for (int np = 0; np <= mt; ++np) {  // two tiles of 8 columns
+        uint32_t o[4];
 #pragma unroll
-        for (int kk = nt / 2; kk <= mt; ++kk) {
-          const uint32_t(&x)[4] = b[nt / 2][kk];
-          const uint32_t y[2] = {x[2 * (nt & 1)], x[2 * (nt & 1) + 1]};
-          mma_f16(c, a[kk], y);
-        }
-        const int j = 8 * nt + 2 * (lane & 3);
-        if (nt < 2 * mt) {
-          const float2 f = *reinterpret_cast<const float2 *>(s_col + 8 * mt * (mt - 1) + j);
-          c[0] *= rt0 * f.x;
-          c[1] *= rt0 * f.y;
-          c[2] *= rt1 * f.x;
-          c[3] *= rt1 * f.y;
-        } else {
-          const float2 d = *reinterpret_cast<const float2 *>(s_rel + j), r = *reinterpret_cast<const float2 *>(s_rho + j);
-          // (above the diagonal the products are zero, and the decays could overflow)
-          c[0] *= r.x * ex2(j <= t ? d0 - d.x : 0.f);
-          c[1] *= r.y * ex2(j + 1 <= t ? d0 - d.y : 0.f);
-          c[2] *= r.x * ex2(j <= t + 8 ? d1 - d.x : 0.f);
-          c[3] *= r.y * ex2(j + 1 <= t + 8 ? d1 - d.y : 0.f);
-        }
-        *reinterpret_cast<uint32_t *>(out + swz(t, nt)) = h2(__floats2half2_rn(c[0], c[1]));
-        *reinterpret_cast<uint32_t *>(out + swz(t + 8, nt)) = h2(__floats2half2_rn(c[2], c[3]));
-      }
+        for (int k = 0; k < 2; ++k) {
+          const int nt = 2 * np + k, j = 8 * nt + 2 * (lane & 3);
+          float c[4] = {};
 #pragma unroll
-      for (int nt = 2 * mt + 2; nt < 8; ++nt) {
-        *reinterpret_cast<uint32_t *>(out + swz(t, nt)) = 0u;
-        *reinterpret_cast<uint32_t *>(out + swz(t + 8, nt)) = 0u;
+          for (int kk = np; kk <= mt; ++kk) {
+            const uint32_t y[2] = {b[np][kk][2 * k], b[np][kk][2 * k + 1]};
+            mma_f16(c, a[kk], y);
+          }
+          if (np < mt) {
+            const float2 f = *reinterpret_cast<const float2 *>(s_col + 8 * mt * (mt - 1) + j);
+            c[0] *= rt0 * f.x;
+            c[1] *= rt0 * f.y;
+            c[2] *= rt1 * f.x;
+            c[3] *= rt1 * f.y;
+          } else {
+            const float2 d = *reinterpret_cast<const float2 *>(s_rel + j), r = *reinterpret_cast<const float2 *>(s_rho + j);
+            // (above the diagonal the products are zero, and the decays could overflow)
+            c[0] *= r.x * ex2(j <= t ? d0 - d.x : 0.f);
+            c[1] *= r.y * ex2(j + 1 <= t ? d0 - d.y : 0.f);
+            c[2] *= r.x * ex2(j <= t + 8 ? d1 - d.x : 0.f);
+            c[3] *= r.y * ex2(j + 1 <= t + 8 ? d1 - d.y : 0.f);
+          }
+          o[2 * k] = h2(__floats2half2_rn(c[0], c[1]));
+          o[2 * k + 1] = h2(__floats2half2_rn(c[2], c[3]));
+        }
+        stmatrix4(im + swz(16 * mt + (lane & 15), 2 * np + (lane >> 4)), o);
       }
+    }
+    __syncwarp();
+    // out by whole lines: written from the fragments, 16 bytes of 8 rows at a time, it would be four times the
+    // requests
+#pragma unroll 4
+    for (int it = 0; it < 16; ++it) {
+      const int x = 32 * it + lane, t = x >> 3, u = (x ^ t) & 7;  // the unit that lies at x
+      const uint4 v = *reinterpret_cast<const uint4 *>(image + 16 * x);
+      reinterpret_cast<uint4 *>(rec + 2 * 8192)[x] = u >> 1 > t >> 4 ? make_uint4(0, 0, 0, 0) : v;
     }
     __syncwarp();
   }
