@@ -33,6 +33,7 @@
 // 14 loads, warp 15 loads T and finds the largest |V| of each chunk.  Hand-overs are mbarriers; every
 // wait is bounded: a timeout makes every role leave and latches SSD_ERR_TIMEOUT.
 #include <cudaTypedefs.h>
+#include <algorithm>
 
 #include "common.cuh"
 #include "delta_mma.cuh"
@@ -69,8 +70,8 @@ constexpr uint32_t OFF_AT = OFF_T + 2 * kT;
 constexpr uint32_t OFF_VG = OFF_AT + 2 * kAT;
 constexpr uint32_t OFF_SB = OFF_VG + kDeep * kVG;  // S operands of the halves: [n][32 p hi, 32 p lo], 128 rows each
 constexpr uint32_t OFF_R = OFF_SB + 2 * kHalf;    // R operands: [token][32 p of each half], 64 rows of hi, 64 of lo
-constexpr uint32_t OFF_MAXS = OFF_R + 2 * 8192;      // largest |S| per chain warp, two chunks
-constexpr uint32_t OFF_MAXV = OFF_MAXS + 64;      // bound of what the chunk adds, per place in the ring
+constexpr uint32_t OFF_MAXS = OFF_R + 2 * 8192;      // largest |S| per chain warp: two chunks, an item's first
+constexpr uint32_t OFF_MAXV = OFF_MAXS + 128;     // bound of what the chunk adds, per place in the ring
 constexpr uint32_t OFF_BAR = OFF_MAXV + 64;
 // A barrier that can complete again before every waiter has seen the phase before has one copy per
 // buffer, so that a parity test never sees two phases at once.
@@ -89,7 +90,8 @@ enum {
   BAR_S = BAR_D1 + 1,              // [2 halves] M R done
   BAR_O = BAR_S + 2,               // A T R done
   BAR_DONE = BAR_O + 1,            // [2] nothing of an issuer's left in flight
-  kNumBars = BAR_DONE + 2
+  BAR_MAX = BAR_DONE + 2,          // [2 halves] the bounds of an item's first state written (4 warps)
+  kNumBars = BAR_MAX + 2
 };
 constexpr uint32_t OFF_MISC = OFF_BAR + 8 * 32;   // [0] TMEM base, [1] abort flag, [2] the same for the last waits
 constexpr uint32_t kSmem = OFF_MISC + 16 + 1024;  // room to align the base to 1024 bytes
@@ -258,12 +260,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int halves = p.P >> 6;
-  const int h = blockIdx.x / halves, ph = blockIdx.x % halves;
-  const int seq = p.order ? p.order[blockIdx.y] : (int)blockIdx.y;
-  const int len = seq_len(p.cu, seq, p.L);
-  const long long base = seq_base(p.cu, seq, p.L);
-  const int nck = (len + C - 1) / C;
+  // Items: 64 state rows of a head of a sequence, the longest sequences' first.  CTA b takes items b, b + gridDim.x,
+  // ..; every role runs through the chunks of all of them (k counts those, c the item's), so that the loads and M
+  // of the next item's first chunks overlap the end of this one's.
+  const uint32_t per_seq = p.H * (p.P >> 6), n_items = p.B * per_seq, step = gridDim.x;
+  const auto seq_at = [&](uint32_t rank) { return p.order ? p.order[rank] : (int)rank; };
+  const auto chunks_of = [&](uint32_t i) { return i < n_items ? (seq_len(p.cu, seq_at(i / per_seq), p.L) + C - 1) / C : 0; };
   const uint32_t bar0 = sb + OFF_BAR;
 #define BAR(i) (bar0 + 8u * (uint32_t)(i))
   uint32_t *misc = reinterpret_cast<uint32_t *>(smem + OFF_MISC);
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(BAR(i), i == BAR_SREADY ? 8 : i >= BAR_MREADY && i < BAR_D1 ? 4 : 1);
+      mbar_init(BAR(i), i == BAR_SREADY ? 8 : i >= BAR_MREADY && i < BAR_D1 || i >= BAR_MAX ? 4 : 1);
     misc[1] = misc[2] = 0;
     fence_mbar_init();
   }
@@ -295,25 +297,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ MMAs of the chains
     Ring<kDeep> r;
     bool ok = true;
-    for (int c = 0; c < nck && ok; ++c, r.next()) {
-      ok = wait(BAR_READY + r.at, r.parity);
-      ok = wait(BAR_SREADY, c & 1) && ok;
-      tc_fence_after();
-      issue_D1(sb + r.at * kTile, sb + OFF_SB, tmem + TM_D1);
-      commit(BAR(BAR_D1));
-      ok = wait2(BAR_MREADY, c) && ok;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        ok = wait(BAR_RREADY + half, c & 1) && ok;
+    int k = 0;
+    for (uint32_t i = blockIdx.x, nck = 0, next; i < n_items + step && ok; i += step, nck = next) {
+      next = chunks_of(i);  // on its way while the item before runs
+      for (uint32_t c = 0; c < nck && ok; ++c, ++k, r.next()) {
+        ok = wait(BAR_READY + r.at, r.parity);
+        ok = wait(BAR_SREADY, k & 1) && ok;
         tc_fence_after();
-        issue_S(tmem + TM_M + 128 * (c & 1), sb + OFF_R, half, tmem + TM_S + 32 * half);
-        commit(BAR(BAR_S + half));
+        issue_D1(sb + r.at * kTile, sb + OFF_SB, tmem + TM_D1);
+        commit(BAR(BAR_D1));
+        ok = wait2(BAR_MREADY, k) && ok;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          ok = wait(BAR_RREADY + half, k & 1) && ok;
+          tc_fence_after();
+          issue_S(tmem + TM_M + 128 * (k & 1), sb + OFF_R, half, tmem + TM_S + 32 * half);
+          commit(BAR(BAR_S + half));
+        }
+        ok = wait2(BAR_AT, k) && ok;
+        issue_O(sb + OFF_AT + (k & 1) * 2048, sb + OFF_R, tmem + TM_O);
+        commit(BAR(BAR_O));
+        commit(BAR(BAR_EMPTY + r.at));
+        ok = __all_sync(0xffffffffu, ok);
       }
-      ok = wait2(BAR_AT, c) && ok;
-      issue_O(sb + OFF_AT + (c & 1) * 2048, sb + OFF_R, tmem + TM_O);
-      commit(BAR(BAR_O));
-      commit(BAR(BAR_EMPTY + r.at));
-      ok = __all_sync(0xffffffffu, ok);
     }
     commit(BAR(BAR_DONE));  // no MMA may still be running when TMEM is released
     settle(BAR_DONE, 0);
@@ -321,17 +327,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ MMAs of M
     Ring<kDeep> r, e;
     bool ok = true;
-    for (int c = 0; c < nck && ok; ++c, r.next()) {
-      ok = wait(BAR_TILE + r.at, r.parity);
-      ok = wait2(BAR_T, c) && ok;
-      if (c >= 2) {  // the M of two chunks before is read
-        ok = wait(BAR_EMPTY + e.at, e.parity) && ok;
-        e.next();
+    int k = 0;
+    for (uint32_t i = blockIdx.x, nck = 0, next; i < n_items + step && ok; i += step, nck = next) {
+      next = chunks_of(i);
+      for (uint32_t c = 0; c < nck && ok; ++c, ++k, r.next()) {
+        ok = wait(BAR_TILE + r.at, r.parity);
+        ok = wait2(BAR_T, k) && ok;
+        if (k >= 2) {  // the M of two chunks before is read
+          ok = wait(BAR_EMPTY + e.at, e.parity) && ok;
+          e.next();
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        issue_M(sb + r.at * kTile, sb + OFF_T + (k & 1) * kT, tmem + TM_M + 128 * (k & 1));
+        commit(BAR(BAR_M + (k & 1)));
       }
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-      issue_M(sb + r.at * kTile, sb + OFF_T + (c & 1) * kT, tmem + TM_M + 128 * (c & 1));
-      commit(BAR(BAR_M + (c & 1)));
     }
     commit(BAR(BAR_DONE + 1));
     settle(BAR_DONE + 1, 0);
@@ -339,42 +349,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ loads of tiles, V, gates, A T
     if (lead) {
       prefetch_tmap(&tm_v);
-      const long long ck0 = p.chunk0 ? p.chunk0[seq] : (long long)seq * nck;
-      const unsigned char *rec = p.records + (ck0 * p.H + h) * kDeltaRecordBytes + kT;
-      const unsigned char *tile = p.tiles + (ck0 * p.G + h / p.hpg) * kDeltaTileBytes;
+      int n = 0, n_at = 0;
       const long long rec_step = p.H * kDeltaRecordBytes, tile_step = p.G * kDeltaTileBytes;
       Ring<kDeep> r, e;  // to load; to become free
-      int n = 0, n_at = 0;
-      // Turn c: tile, V and gates of chunk c, into the place of chunk c - 3; A T of chunk c - 1 (and in
-      // turn 0 of chunk 0), whose two places are free then too.  The last turn loads A T alone.
-      for (int c = 0; c <= nck; ++c) {
-        if (c >= kDeep) {
-          if (!wait(BAR_EMPTY + e.at, e.parity)) break;
-          e.next();
-        }
-        if (c < nck) {
+      const unsigned char *before = nullptr;  // A T of the chunk before
+      const auto load_at = [&](const unsigned char *src) {
+        const uint32_t at = BAR(BAR_AT + (n_at & 1));
+        mbar_arrive_expect_tx(at, kAT);
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j)  // the two places alternate by 16 rows
+          bulk_load(sb + OFF_AT + (n_at & 1) * 2048 + j * 4096, src + j * 2048, 2048, at);
+        ++n_at;
+      };
+      // Chunk k's turn: its tile, V and gates, into the place of chunk k - 3; A T of chunk k - 1 (and in turn 0 of
+      // chunk 0), whose two places are free then too.  A last turn loads A T alone.
+      bool ok = true;
+      for (uint32_t i = blockIdx.x; i < n_items && ok; i += step) {
+        const uint32_t rank = i / per_seq, hp = i - rank * per_seq;  // 64 rows of a head: h P / 64 + ..
+        const int seq = seq_at(rank), h = hp >> (p.P > 64), nck = (seq_len(p.cu, seq, p.L) + C - 1) / C;
+        const long long base = seq_base(p.cu, seq, p.L);
+        const long long ck0 = p.chunk0 ? p.chunk0[seq] : (long long)seq * nck;
+        const unsigned char *rec = p.records + (ck0 * p.H + h) * kDeltaRecordBytes + kT;
+        const unsigned char *tile = p.tiles + (ck0 * p.G + h / p.hpg) * kDeltaTileBytes;
+        for (int c = 0; c < nck; ++c, rec += rec_step, tile += tile_step) {
+          if (n >= kDeep) {
+            ok = wait(BAR_EMPTY + e.at, e.parity);
+            if (!ok) break;
+            e.next();
+          }
           const uint32_t vg = BAR(BAR_VG + r.at), tb = BAR(BAR_TILE + r.at), dst = sb + OFF_VG + r.at * kVG;
           mbar_arrive_expect_tx(vg, 8192 + 768);
           // 64 token rows, the ones after the sequence's end among them (they are not used)
-          tma_load_2d(dst, &tm_v, h * p.P + 64 * ph, (int)(base + c * C), vg);
+          tma_load_2d(dst, &tm_v, (int)(64 * hp), (int)(base + c * C), vg);
           // V is the caller's; tiles and records are the front end's, which may still be running
           // (programmatic dependent launch)
-          if (c == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+          if (n == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
           mbar_arrive_expect_tx(tb, (uint32_t)kDeltaTileBytes);
-          bulk_load(sb + r.at * kTile, tile + c * tile_step, (uint32_t)kDeltaTileBytes, tb);
-          bulk_load(dst + OFF_BETA, rec + c * rec_step + kAT, 768, vg);
+          bulk_load(sb + r.at * kTile, tile, (uint32_t)kDeltaTileBytes, tb);
+          bulk_load(dst + OFF_BETA, rec + kAT, 768, vg);
           r.next();
+          if (n != 1) load_at(n == 0 ? rec : before);
+          before = rec;
           ++n;
         }
-        if (c != 1 && n_at < nck) {
-          const uint32_t at = BAR(BAR_AT + (n_at & 1));
-          mbar_arrive_expect_tx(at, kAT);
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i)  // the two places alternate by 16 rows
-            bulk_load(sb + OFF_AT + (n_at & 1) * 2048 + i * 4096, rec + n_at * rec_step + i * 2048, 2048, at);
-          ++n_at;
-        }
       }
+      if (ok && n >= 2 && (n < kDeep || wait(BAR_EMPTY + e.at, e.parity))) load_at(before);
       // every load must land before the CTA may exit
       for (int k = 0; k < kDeep; ++k)
         if (k < n) {
@@ -388,22 +407,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 15) {
     // ------------------------------------------------------------------ loads of T; the largest |V| of each chunk,
     // times the largest |beta| / 2 where that is above one
-    const long long ck0 = p.chunk0 ? p.chunk0[seq] : (long long)seq * nck;
-    const unsigned char *rec = p.records + (ck0 * p.H + h) * kDeltaRecordBytes;
-    if (lead && nck > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    uint32_t i = blockIdx.x - step;  // the item of the T to load, its chunks, the chunk
+    int len = 0, nck = 0, c = 0;
+    const unsigned char *rec = nullptr;
+    int rows = 0, rows_next = 0;     // tokens of chunk k, of chunk k + 1
     Ring<kDeep> r;
     int n = 0;
-    // Turn c: the bound of chunk c, then T of chunk c + 2 over that of chunk c, once M has taken it
-    for (int c = -2; c < nck; ++c) {
-      if (c >= 0) {
+    // Turn k: the bound of chunk k, then T of chunk k + 2 over that of chunk k, once M has taken it
+    for (int k = -2; k < 0 || rows > 0; ++k) {
+      while (c == nck && i + step < n_items) {  // the next item that has chunks
+        i += step;
+        const uint32_t rank = i / per_seq;
+        const int seq = seq_at(rank), h = (i - rank * per_seq) >> (p.P > 64);
+        len = seq_len(p.cu, seq, p.L);
+        nck = (len + C - 1) / C;
+        c = 0;
+        rec = p.records + ((p.chunk0 ? p.chunk0[seq] : (long long)seq * nck) * p.H + h) * kDeltaRecordBytes;
+      }
+      if (k >= 0) {
         bool ok = wait(BAR_VG + r.at, r.parity);
         ok = wait(BAR_TILE + r.at, r.parity) && ok;
         const unsigned char *stage = smem + OFF_VG + r.at * kVG;
-        const int rows = min(C, len - c * C);
         uint32_t top = 0;
-#pragma unroll 4
-        for (int i = lane >> 3; i < rows; i += 4) {
-          const uint4 u = *reinterpret_cast<const uint4 *>(stage + i * 128 + (lane & 7) * 16);
+#pragma unroll 2
+        for (int t = lane >> 3; t < rows; t += 4) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(stage + t * 128 + (lane & 7) * 16);
           top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
                                        __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
         }
@@ -416,13 +444,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         r.next();
-        if (c + 2 < nck) ok = wait2(BAR_M, c) && ok;
+        if (c < nck) ok = wait2(BAR_M, k) && ok;
         if (!__all_sync(0xffffffffu, ok)) break;
       }
-      if (lead && c + 2 < nck) {
-        const uint32_t t = BAR(BAR_T + (c & 1));
-        mbar_arrive_expect_tx(t, kT);
-        bulk_load(sb + OFF_T + (c & 1) * kT, rec + (long long)(c + 2) * p.H * kDeltaRecordBytes, kT, t);
+      rows = rows_next;
+      rows_next = 0;
+      if (c < nck) {
+        if (k == -2 && lead) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (lead) {
+          const uint32_t t = BAR(BAR_T + (k & 1));
+          mbar_arrive_expect_tx(t, kT);
+          bulk_load(sb + OFF_T + (k & 1) * kT, rec, kT, t);
+        }
+        rows_next = min(C, len - c * C);
+        rec += p.H * kDeltaRecordBytes;
+        ++c;
         ++n;
       }
       __syncwarp();
@@ -434,15 +470,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ M, its columns times
     // rho_j 2^{cs_C - cs_j}, into its operand
     Ring<kDeep> r;
-    for (int c = 0; c < nck; ++c, r.next()) {
-      bool ok = wait(BAR_VG + r.at, r.parity);  // the factors
-      ok = wait2(BAR_M, c) && ok;
-      if (!__all_sync(0xffffffffu, ok)) break;
+    bool ok = true;
+    int k = 0;
+    for (uint32_t i = blockIdx.x, nck = 0, next; i < n_items + step && ok; i += step, nck = next) {
+    next = chunks_of(i);
+    for (uint32_t c = 0; c < nck; ++c, ++k, r.next()) {
+      ok = wait(BAR_VG + r.at, r.parity);  // the factors
+      ok = wait2(BAR_M, k) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
       tc_fence_after();
       const float4 *f = reinterpret_cast<const float4 *>(smem + OFF_VG + r.at * kVG + OFF_END);
 #pragma unroll 1
       for (int b = 0; b < 2; ++b) {
-        const uint32_t at = tmem + TM_M + 128 * (c & 1) + 32 * b + lane_off;
+        const uint32_t at = tmem + TM_M + 128 * (k & 1) + 32 * b + lane_off;
         float m[32], e[32];
         uint32_t hv[16], lv[16];
         tmem_ld32(at, m);
@@ -461,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(BAR_MREADY + (c & 1)));
+      if (lane == 0) mbar_arrive(BAR(BAR_MREADY + (k & 1)));
+    }
     }
   } else {
     // ------------------------------------------------------------------ the chains
@@ -469,15 +511,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = 16 * q4 + (lane >> 2);   // this thread's tokens of D1 and O: row, row + 8
     const int col = 2 * (lane & 3);          // its columns of them: 8 b + col, 8 b + col + 1, b = 0 .. 3
     const int n = 32 * q4 + lane;            // state column of this thread
-    const long long soff = (((long long)seq * p.H + h) * p.P + 64 * ph + 32 * hf) * kDState + n;
-    uint32_t *max_s = reinterpret_cast<uint32_t *>(smem + OFF_MAXS) + 8 * hf;
+    uint32_t *max_s = reinterpret_cast<uint32_t *>(smem + OFF_MAXS) + 12 * hf;
     const uint32_t t_d1 = tmem + TM_D1 + 64 * hf, t_s = tmem + TM_S + 32 * hf, t_o = tmem + TM_O + 32 * hf;
     float2 S[16];  // the state, times sc.x
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      S[i].x = p.h0 ? p.h0[soff + (2 * i) * kDState] : 0.f;
-      S[i].y = p.h0 ? p.h0[soff + (2 * i + 1) * kDState] : 0.f;
-    }
+    int len = 0;             // of the item: tokens, the first of them's row, and h P + the first state row
+    long long base = 0;
+    int hp = 0;
     const auto publish_max = [&](int buf) {
       float top = 0.f;
 #pragma unroll
@@ -489,12 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint4 a = *reinterpret_cast<const uint4 *>(max_s + 4 * buf);
       return __uint_as_float(max(max(a.x, a.y), max(a.z, a.w)));
     };
-    publish_max(1);
-    named_bar(1 + hf, 128);
-    float m = read_max(1);  // bounds the state as described at state_scale
-    float2 sc = state_scale(m);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) S[i] = __fmul2_rn(S[i], make_float2(sc.x, sc.x));
+    float m;    // bounds the state as described at state_scale
+    float2 sc;
     uint32_t v[2][4];                  // the chunk's V, pairs
     float2 hold[2][4];                 // 2^cs Q S^T of the chunk whose y is still to come
     float gamma[2], beta[2], rho_k[2], rho_q[2], gamma_end = 0.f, vmax = 0.f;  // of the chunk
@@ -524,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ring.next();
       return ok;
     };
-    const auto put_y = [&](int c) {  // y of chunk c
-      wait(BAR_O, c & 1);
+    const auto put_y = [&](int c, int k) {  // y of the item's chunk c, the k-th in all
+      wait(BAR_O, k & 1);
       __syncwarp();
       tc_fence_after();
       float o[16];
@@ -535,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int t = c * C + row + 8 * i;
-        const long long yo = (base + t) * p.ys + (long long)h * p.P + 64 * ph + 32 * hf + col;
+        const long long yo = (base + t) * p.ys + hp + 32 * hf + col;
         const bool store = t < len && in_bounds(yo + 25, p.y_extent, p.err);
         const float2 r2 = make_float2(rho_y[i], rho_y[i]);
         uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.y) + yo);
@@ -547,8 +582,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    bool ok = nck == 0 || load_rows(0);
-    for (int c = 0; c < nck; ++c) {
+    bool ok = true;
+    int k = 0, fulls = 0;  // chunks; items with chunks
+    int seq = 0, hp_next = 0;  // of the next item
+    for (uint32_t i = blockIdx.x; i < n_items + step && ok; i += step) {
+    const int seq_now = seq;
+    hp = hp_next;
+    if (i < n_items) {  // on its way while the item before runs
+      const uint32_t rank = i / per_seq;
+      seq = seq_at(rank);
+      hp_next = 64 * (i - rank * per_seq);
+    }
+    if (i < step) continue;
+    len = seq_len(p.cu, seq_now, p.L);
+    base = seq_base(p.cu, seq_now, p.L);
+    const int nck = (len + C - 1) / C;
+    const long long soff = ((long long)seq_now * p.H * p.P + hp + 32 * hf) * kDState + n;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) S[j] = make_float2(0.f, 0.f);
+    if (p.h0) {
+      const float *src = p.h0 + soff;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) S[j] = make_float2(src[(2 * j) * kDState], src[(2 * j + 1) * kDState]);
+    }
+    m = 0.f;
+    if (p.h0 && nck > 0) {
+      publish_max(2);
+      if (lead) mbar_arrive(BAR(BAR_MAX + hf));
+      ok = wait(BAR_MAX + hf, fulls++ & 1);
+      __syncwarp();
+      m = read_max(2);
+    }
+    sc = state_scale(m);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) S[j] = __fmul2_rn(S[j], make_float2(sc.x, sc.x));
+    if (nck > 0) ok = load_rows(0) && ok;
+    for (int c = 0; c < nck; ++c, ++k) {
       // S into its operand
       unsigned char *so = smem + OFF_SB + hf * kHalf;
 #pragma unroll
@@ -564,11 +633,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lead) mbar_arrive(BAR(BAR_SREADY));
       // while K S^T runs: y of the chunk before, the bound of |S|
-      if (c > 0) put_y(c - 1);
-      publish_max(c & 1);
+      if (c > 0) put_y(c - 1, k - 1);
+      publish_max(k & 1);
       const float2 rsc = state_scale(fmaxf(m, vmax));
       back_o = rsc.y;
-      ok = wait(BAR_D1, c & 1) && ok;
+      ok = wait(BAR_D1, k & 1) && ok;
       __syncwarp();
       tc_fence_after();
       {
@@ -613,11 +682,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // S = gamma_end S + M R, in the next chunk's scale; while the product runs: the next chunk's rows
       const float decay = gamma_end * sc.y, bound = vmax;
       if (c + 1 < nck) ok = load_rows(c + 1) && ok;
-      ok = wait(BAR_S + hf, c & 1) && ok;
+      ok = wait(BAR_S + hf, k & 1) && ok;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      m = fmaf(decay, read_max(c & 1), bound);
+      m = fmaf(decay, read_max(k & 1), bound);
       sc = state_scale(m);
       const float ge = decay * sc.x, yn = rsc.y * sc.x;
       const float2 ge2 = make_float2(ge, ge), y2 = make_float2(yn, yn);
@@ -632,14 +701,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 8; ++i) S[8 * x + i] = __ffma2_rn(y2, make_float2(d[2 * i], d[2 * i + 1]), S[8 * x + i]);
       }
     }
-    if (ok) {
-      if (nck > 0) put_y(nck - 1);
-      if (p.h_final) {
+    if (ok && p.h_final && in_bounds(soff + 31 * kDState, p.state_extent, p.err)) {
+      float *dst = p.h_final + soff;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (in_bounds(soff + (long long)i * kDState, p.state_extent, p.err))
-            p.h_final[soff + (long long)i * kDState] = sc.y * (i & 1 ? S[i / 2].y : S[i / 2].x);
-      }
+      for (int j = 0; j < 32; ++j) dst[j * kDState] = sc.y * (j & 1 ? S[j / 2].y : S[j / 2].x);
+    }
+    if (ok && nck > 0) put_y(nck - 1, k - 1);
     }
   }
 
@@ -684,7 +751,7 @@ cudaError_t launch_delta_chunks(const DeltaPlan &p, cudaStream_t s) {
   // a programmatic dependent of the front end: its set-up and first loads of V overlap the front
   // end's tail
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)(p.H * (p.P / 64)), (unsigned)p.B);
+  lc.gridDim = dim3((unsigned)std::min<long long>((long long)p.B * p.H * (p.P / 64), 148));
   lc.blockDim = dim3(kThreads);
   lc.dynamicSmemBytes = kSmem;
   lc.stream = s;
