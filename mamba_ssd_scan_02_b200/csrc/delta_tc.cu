@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait(BAR_TILE + r.at, r.parity) && ok;
         const unsigned char *stage = smem + OFF_VG + r.at * kVG;
         uint32_t top = 0;
-#pragma unroll 2
+#pragma unroll 4
         for (int t = lane >> 3; t < rows; t += 4) {
           const uint4 u = *reinterpret_cast<const uint4 *>(stage + t * 128 + (lane & 7) * 16);
           top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
@@ -511,6 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = 16 * q4 + (lane >> 2);   // this thread's tokens of D1 and O: row, row + 8
     const int col = 2 * (lane & 3);          // its columns of them: 8 b + col, 8 b + col + 1, b = 0 .. 3
     const int n = 32 * q4 + lane;            // state column of this thread
+    // swizzled places: unit k of the thread's row of the S operand at s_at ^ 16 k, columns 8 b of its rows of V and R
+    // at r_at ^ 16 b
+    const uint32_t s_at = OFF_SB + hf * kHalf + swz(n, 0), r_at = swz(row, 4 * hf) + 2 * col;
     uint32_t *max_s = reinterpret_cast<uint32_t *>(smem + OFF_MAXS) + 12 * hf;
     const uint32_t t_d1 = tmem + TM_D1 + 64 * hf, t_s = tmem + TM_S + 32 * hf, t_o = tmem + TM_O + 32 * hf;
     float2 S[16];  // the state, times sc.x
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         rho_q[i] = rho(OFF_RHOQ)[t];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const uint32_t u = *reinterpret_cast<const uint32_t *>(stage + swz(t, 4 * hf + b) + 2 * col);
+          const uint32_t u = *reinterpret_cast<const uint32_t *>(stage + (r_at ^ 16 * b) + 1024 * i);
           v[i][b] = live ? u : 0u;
         }
       }
@@ -619,14 +622,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (nck > 0) ok = load_rows(0) && ok;
     for (int c = 0; c < nck; ++c, ++k) {
       // S into its operand
-      unsigned char *so = smem + OFF_SB + hf * kHalf;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int j = 0; j < 4; ++j) {
         uint32_t hv[4], lv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split2(S[4 * k + i], hv[i], lv[i]);
-        *reinterpret_cast<uint4 *>(so + swz(n, k)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-        *reinterpret_cast<uint4 *>(so + swz(n, 4 + k)) = make_uint4(lv[0], lv[1], lv[2], lv[3]);
+        for (int x = 0; x < 4; ++x) split2(S[4 * j + x], hv[x], lv[x]);
+        *reinterpret_cast<uint4 *>(smem + (s_at ^ 16 * j)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+        *reinterpret_cast<uint4 *>(smem + (s_at ^ 16 * (4 + j))) = make_uint4(lv[0], lv[1], lv[2], lv[3]);
       }
       fence_proxy_async();
       tc_fence_before();
@@ -656,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 ks = __fadd2_rn(make_float2(d[x], d[x + 1]), make_float2(e[x], e[x + 1]));
             uint32_t hv, lv;
             split2(__fmul2_rn(b2, __ffma2_rn(k2, ks, vp)), hv, lv);
-            unsigned char *o = smem + OFF_R + swz(row + 8 * i, 4 * hf + b) + 2 * col;
+            unsigned char *o = smem + OFF_R + (r_at ^ 16 * b) + 1024 * i;
             *reinterpret_cast<uint32_t *>(o) = hv;
             *reinterpret_cast<uint32_t *>(o + 8192) = lv;
           }
