@@ -233,8 +233,11 @@ ssd_status_t mamba2_mixer_forward(const ssd_mixer_config_t *cfg, const ssd_mixer
  *
  * per batch row and head h; the heads of a group share q and k (g = h / (H/G)).  q, k and v are
  * the rows after any convolution and activation.  The state has the layout of the scan's,
- * [B, H, P, N] fp32, so the state cache below serves both.  alpha_t in (0, 1] (A <= 0) and
- * beta_t |k^_t|^2 <= 2 keep the state bounded; other values are computed as they stand. */
+ * [B, H, P, N] fp32, so the state cache below serves both.  alpha_t in [0, 1] (A <= 0) and
+ * 0 <= beta_t |k^_t|^2 <= 2 keep the state bounded.  The chunked kernels need both (beyond them their 16-bit
+ * operands can overflow, to NaN); the recurrence and the decode step compute other values as they
+ * stand.  A NaN or an infinity in a token reaches every later y and state of its sequence and head (q: its
+ * own y), and on the chunked kernels those of the token's chunk of 64 that come before it, too. */
 typedef struct {
   int batch;        /* B >= 1 */
   int seqlen;       /* L >= 0 tokens in this call (0: h0, or zeros, goes to h_final); ignored by
@@ -251,8 +254,9 @@ typedef struct {
   int beta_sigmoid; /* 1: beta = beta_scale * sigmoid(b); 0: beta = beta_scale * b */
   float beta_scale; /* 1, or 2 to allow negative eigenvalues of the transition */
   ssd_dtype_t io_dtype; /* dtype of q, k, v, dt, b and y */
-  ssd_kernel_t kernel;  /* TENSOR: the chunked kernel (bf16 only; UNSUPPORTED otherwise); SIMT: the
-                           token recurrence in fp32; AUTO: whichever is faster for the lengths */
+  ssd_kernel_t kernel;  /* TENSOR: the chunked kernels (bf16 only; UNSUPPORTED otherwise); SIMT: the
+                           recurrence in fp32; AUTO: whichever is faster for the lengths, the chunked
+                           ones only with qk_norm, beta_sigmoid and beta_scale in [0, 2] */
 } ssd_delta_config_t;
 
 typedef struct {

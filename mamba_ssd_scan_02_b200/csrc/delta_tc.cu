@@ -293,7 +293,252 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
 
   const bool lead = lane == 0;
-  if (warp == 12) {
+  if (warp < 8) {
+    // ------------------------------------------------------------------ the chains
+    const int hf = warp >> 2;                // half: state rows (columns of S and O) 32 hf ..
+    const int row = 16 * q4 + (lane >> 2);   // this thread's tokens of D1 and O: row, row + 8
+    const int col = 2 * (lane & 3);          // its columns of them: 8 b + col, 8 b + col + 1, b = 0 .. 3
+    const int n = 32 * q4 + lane;            // state column of this thread
+    // swizzled places: unit k of the thread's row of the S operand at s_at ^ 16 k, columns 8 b of its rows of V and R
+    // at r_at ^ 16 b
+    const uint32_t s_at = OFF_SB + hf * kHalf + swz(n, 0), r_at = swz(row, 4 * hf) + 2 * col;
+    uint32_t *max_s = reinterpret_cast<uint32_t *>(smem + OFF_MAXS) + 12 * hf;
+    const uint32_t t_d1 = tmem + TM_D1 + 64 * hf, t_s = tmem + TM_S + 32 * hf, t_o = tmem + TM_O + 32 * hf;
+    float2 S[16];  // the state, times sc.x
+    int len = 0;             // of the item: tokens, the first of them's row, and h P + the first state row
+    long long base = 0;
+    int hp = 0;
+    const auto publish_max = [&](int buf) {
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(fabsf(S[i].x), fabsf(S[i].y)));
+      const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+      if (lane == 0) max_s[4 * buf + q4] = bits;
+    };
+    const auto read_max = [&](int buf) {
+      const uint4 a = *reinterpret_cast<const uint4 *>(max_s + 4 * buf);
+      return __uint_as_float(max(max(a.x, a.y), max(a.z, a.w)));
+    };
+    float m;    // bounds the state as described at state_scale
+    float2 sc;
+    uint32_t v[2][4];                  // the chunk's V, pairs
+    float2 hold[2][4];                 // 2^cs Q S^T of the chunk whose y is still to come
+    float gamma[2], beta[2], rho_k[2], rho_q[2], gamma_end = 0.f, vmax = 0.f;  // of the chunk
+    float back_o = 0.f, rho_y[2];      // of the y to come
+    Ring<kDeep> ring;  // of the rows to load next
+    const auto load_rows = [&](int c) {
+      const unsigned char *stage = smem + OFF_VG + ring.at * kVG;
+      const auto arr = [&](uint32_t off) { return reinterpret_cast<const float *>(stage + off); };
+      const auto rho = [&](uint32_t off) { return reinterpret_cast<const float *>(smem + ring.at * kTile + off); };
+      const bool ok = wait(BAR_READY + ring.at, ring.parity);
+      vmax = reinterpret_cast<const float *>(smem + OFF_MAXV)[ring.at];
+      gamma_end = arr(OFF_GAMMA)[C - 1];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = row + 8 * i;
+        const bool live = c * C + t < len;  // (the rows after may hold anything)
+        gamma[i] = arr(OFF_GAMMA)[t];
+        beta[i] = live ? arr(OFF_BETA)[t] : 0.f;
+        rho_k[i] = rho(OFF_RHOK)[t];
+        rho_q[i] = rho(OFF_RHOQ)[t];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t u = *reinterpret_cast<const uint32_t *>(stage + (r_at ^ 16 * b) + 1024 * i);
+          v[i][b] = live ? u : 0u;
+        }
+      }
+      ring.next();
+      return ok;
+    };
+    const auto put_y = [&](int c, int k) {  // y of the item's chunk c, the k-th in all
+      wait(BAR_O, k & 1);
+      __syncwarp();
+      tc_fence_after();
+      float o[16];
+      tmem_ld_rows(t_o + lane_off + (16u << 16), o);
+      tmem_ld_wait();
+      const float2 b2 = make_float2(back_o, back_o);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = c * C + row + 8 * i;
+        const long long yo = (base + t) * p.ys + hp + 32 * hf + col;
+        const bool store = t < len && in_bounds(yo + 25, p.y_extent, p.err);
+        const float2 r2 = make_float2(rho_y[i], rho_y[i]);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.y) + yo);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const float2 f = __fmul2_rn(r2, __ffma2_rn(b2, make_float2(o[4 * b + 2 * i], o[4 * b + 2 * i + 1]), hold[i][b]));
+          const __nv_bfloat162 x = __float22bfloat162_rn(f);
+          if (store) dst[4 * b] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+      }
+    };
+    bool ok = true;
+    int k = 0, fulls = 0;  // chunks; items with chunks
+    int seq = 0, hp_next = 0;  // of the next item
+    for (uint32_t i = blockIdx.x; i < n_items + step && ok; i += step) {
+      const int seq_now = seq;
+      hp = hp_next;
+      if (i < n_items) {  // on its way while the item before runs
+        const uint32_t rank = i / per_seq;
+        seq = seq_at(rank);
+        hp_next = 64 * (i - rank * per_seq);
+      }
+      if (i < step) continue;
+      len = seq_len(p.cu, seq_now, p.L);
+      base = seq_base(p.cu, seq_now, p.L);
+      const int nck = (len + C - 1) / C;
+      const long long soff = ((long long)seq_now * p.H * p.P + hp + 32 * hf) * kDState + n;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) S[j] = make_float2(0.f, 0.f);
+      if (p.h0) {
+        const float *src = p.h0 + soff;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) S[j] = make_float2(src[(2 * j) * kDState], src[(2 * j + 1) * kDState]);
+      }
+      m = 0.f;
+      if (p.h0 && nck > 0) {
+        publish_max(2);
+        if (lead) mbar_arrive(BAR(BAR_MAX + hf));
+        ok = wait(BAR_MAX + hf, fulls++ & 1);
+        __syncwarp();
+        m = read_max(2);
+      }
+      sc = state_scale(m);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) S[j] = __fmul2_rn(S[j], make_float2(sc.x, sc.x));
+      if (nck > 0) ok = load_rows(0) && ok;
+      for (int c = 0;; ++c, ++k) {
+        if (c < nck) {
+          // S into its operand
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t hv[4], lv[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) split2(S[4 * j + x], hv[x], lv[x]);
+            *reinterpret_cast<uint4 *>(smem + (s_at ^ 16 * j)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+            *reinterpret_cast<uint4 *>(smem + (s_at ^ 16 * (4 + j))) = make_uint4(lv[0], lv[1], lv[2], lv[3]);
+          }
+          fence_proxy_async();
+          tc_fence_before();
+          __syncwarp();
+          if (lead) mbar_arrive(BAR(BAR_SREADY));
+        } else if (p.h_final && in_bounds(soff + 31 * kDState, p.state_extent, p.err)) {
+          float *dst = p.h_final + soff;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) dst[j * kDState] = sc.y * (j & 1 ? S[j / 2].y : S[j / 2].x);
+        }
+        // while K S^T runs: y of the chunk before, the bound of |S|
+        if (c > 0) put_y(c - 1, k - 1);
+        if (c == nck) break;
+        publish_max(k & 1);
+        const float2 rsc = state_scale(fmaxf(m, vmax));
+        back_o = rsc.y;
+        ok = wait(BAR_D1, k & 1) && ok;
+        __syncwarp();
+        tc_fence_after();
+        {
+          float d[16], e[16];
+          tmem_ld_rows(t_d1 + lane_off, d);
+          tmem_ld_rows(t_d1 + 32 + lane_off, e);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float g = -gamma[i] * sc.y * rho_k[i], bt = beta[i] * rsc.x;
+            const float2 k2 = make_float2(g, g), b2 = make_float2(bt, bt);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const int x = 4 * b + 2 * i;
+              const float2 vp = make_float2(__uint_as_float(v[i][b] << 16), __uint_as_float(v[i][b] & 0xffff0000u));
+              const float2 ks = __fadd2_rn(make_float2(d[x], d[x + 1]), make_float2(e[x], e[x + 1]));
+              uint32_t hv, lv;
+              split2(__fmul2_rn(b2, __ffma2_rn(k2, ks, vp)), hv, lv);
+              unsigned char *o = smem + OFF_R + (r_at ^ 16 * b) + 1024 * i;
+              *reinterpret_cast<uint32_t *>(o) = hv;
+              *reinterpret_cast<uint32_t *>(o + 8192) = lv;
+            }
+          }
+          tmem_ld_rows(t_d1 + lane_off + (16u << 16), d);
+          tmem_ld_rows(t_d1 + 32 + lane_off + (16u << 16), e);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float g = gamma[i] * sc.y;
+            rho_y[i] = rho_q[i];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const int x = 4 * b + 2 * i;
+              hold[i][b] = __fmul2_rn(make_float2(g, g), __fadd2_rn(make_float2(d[x], d[x + 1]), make_float2(e[x], e[x + 1])));
+            }
+          }
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lead) mbar_arrive(BAR(BAR_RREADY + hf));
+        // S = gamma_end S + M R, in the next chunk's scale; while the product runs: the next chunk's rows
+        const float decay = gamma_end * sc.y, bound = vmax;
+        if (c + 1 < nck) ok = load_rows(c + 1) && ok;
+        ok = wait(BAR_S + hf, k & 1) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        m = fmaf(decay, read_max(k & 1), bound);
+        sc = state_scale(m);
+        const float ge = decay * sc.x, yn = rsc.y * sc.x;
+        const float2 ge2 = make_float2(ge, ge), y2 = make_float2(yn, yn);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[i] = __fmul2_rn(S[i], ge2);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float d[16];
+          tmem_ld16(t_s + 16 * x + lane_off, d);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) S[8 * x + i] = __ffma2_rn(y2, make_float2(d[2 * i], d[2 * i + 1]), S[8 * x + i]);
+        }
+      }
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------------ M, its columns times
+    // rho_j 2^{cs_C - cs_j}, into its operand
+    Ring<kDeep> r;
+    bool ok = true;
+    int k = 0;
+    for (uint32_t i = blockIdx.x, nck = 0, next; i < n_items + step && ok; i += step, nck = next) {
+      next = chunks_of(i);
+      for (uint32_t c = 0; c < nck; ++c, ++k, r.next()) {
+        ok = wait(BAR_VG + r.at, r.parity);  // the factors
+        ok = wait2(BAR_M, k) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const float4 *f = reinterpret_cast<const float4 *>(smem + OFF_VG + r.at * kVG + OFF_END);
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t at = tmem + TM_M + 128 * (k & 1) + 32 * b + lane_off;
+          float m[32], e[32];
+          uint32_t hv[16], lv[16];
+          tmem_ld32(at, m);
+          tmem_ld32(at + 64, e);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 x = f[8 * b + j];
+            const auto sum = [&](int i) { return __fadd2_rn(make_float2(m[i], m[i + 1]), make_float2(e[i], e[i + 1])); };
+            split2(__fmul2_rn(sum(4 * j), make_float2(x.x, x.y)), hv[2 * j], lv[2 * j]);
+            split2(__fmul2_rn(sum(4 * j + 2), make_float2(x.z, x.w)), hv[2 * j + 1], lv[2 * j + 1]);
+          }
+          tmem_st16(at, hv);
+          tmem_st16(at + 16, lv);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(BAR_MREADY + (k & 1)));
+      }
+    }
+  } else if (warp == 12) {
     // ------------------------------------------------------------------ MMAs of the chains
     Ring<kDeep> r;
     bool ok = true;
@@ -404,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = max(0, n_at - 2); k < n_at; ++k) settle(BAR_AT + (k & 1), (k >> 1) & 1);
     }
     __syncwarp();
-  } else if (warp == 15) {
+  } else {
     // ------------------------------------------------------------------ loads of T; the largest |V| of each chunk,
     // times the largest |beta| / 2 where that is above one
     uint32_t i = blockIdx.x - step;  // the item of the T to load, its chunks, the chunk
@@ -466,250 +711,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lead)
       for (int k = max(0, n - 2); k < n; ++k) settle(BAR_T + (k & 1), (k >> 1) & 1);
     __syncwarp();
-  } else if (warp >= 8) {
-    // ------------------------------------------------------------------ M, its columns times
-    // rho_j 2^{cs_C - cs_j}, into its operand
-    Ring<kDeep> r;
-    bool ok = true;
-    int k = 0;
-    for (uint32_t i = blockIdx.x, nck = 0, next; i < n_items + step && ok; i += step, nck = next) {
-    next = chunks_of(i);
-    for (uint32_t c = 0; c < nck; ++c, ++k, r.next()) {
-      ok = wait(BAR_VG + r.at, r.parity);  // the factors
-      ok = wait2(BAR_M, k) && ok;
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const float4 *f = reinterpret_cast<const float4 *>(smem + OFF_VG + r.at * kVG + OFF_END);
-#pragma unroll 1
-      for (int b = 0; b < 2; ++b) {
-        const uint32_t at = tmem + TM_M + 128 * (k & 1) + 32 * b + lane_off;
-        float m[32], e[32];
-        uint32_t hv[16], lv[16];
-        tmem_ld32(at, m);
-        tmem_ld32(at + 64, e);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float4 x = f[8 * b + j];
-          const auto sum = [&](int i) { return __fadd2_rn(make_float2(m[i], m[i + 1]), make_float2(e[i], e[i + 1])); };
-          split2(__fmul2_rn(sum(4 * j), make_float2(x.x, x.y)), hv[2 * j], lv[2 * j]);
-          split2(__fmul2_rn(sum(4 * j + 2), make_float2(x.z, x.w)), hv[2 * j + 1], lv[2 * j + 1]);
-        }
-        tmem_st16(at, hv);
-        tmem_st16(at + 16, lv);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(BAR_MREADY + (k & 1)));
-    }
-    }
-  } else {
-    // ------------------------------------------------------------------ the chains
-    const int hf = warp >> 2;                // half: state rows (columns of S and O) 32 hf ..
-    const int row = 16 * q4 + (lane >> 2);   // this thread's tokens of D1 and O: row, row + 8
-    const int col = 2 * (lane & 3);          // its columns of them: 8 b + col, 8 b + col + 1, b = 0 .. 3
-    const int n = 32 * q4 + lane;            // state column of this thread
-    // swizzled places: unit k of the thread's row of the S operand at s_at ^ 16 k, columns 8 b of its rows of V and R
-    // at r_at ^ 16 b
-    const uint32_t s_at = OFF_SB + hf * kHalf + swz(n, 0), r_at = swz(row, 4 * hf) + 2 * col;
-    uint32_t *max_s = reinterpret_cast<uint32_t *>(smem + OFF_MAXS) + 12 * hf;
-    const uint32_t t_d1 = tmem + TM_D1 + 64 * hf, t_s = tmem + TM_S + 32 * hf, t_o = tmem + TM_O + 32 * hf;
-    float2 S[16];  // the state, times sc.x
-    int len = 0;             // of the item: tokens, the first of them's row, and h P + the first state row
-    long long base = 0;
-    int hp = 0;
-    const auto publish_max = [&](int buf) {
-      float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(fabsf(S[i].x), fabsf(S[i].y)));
-      const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-      if (lane == 0) max_s[4 * buf + q4] = bits;
-    };
-    const auto read_max = [&](int buf) {
-      const uint4 a = *reinterpret_cast<const uint4 *>(max_s + 4 * buf);
-      return __uint_as_float(max(max(a.x, a.y), max(a.z, a.w)));
-    };
-    float m;    // bounds the state as described at state_scale
-    float2 sc;
-    uint32_t v[2][4];                  // the chunk's V, pairs
-    float2 hold[2][4];                 // 2^cs Q S^T of the chunk whose y is still to come
-    float gamma[2], beta[2], rho_k[2], rho_q[2], gamma_end = 0.f, vmax = 0.f;  // of the chunk
-    float back_o = 0.f, rho_y[2];      // of the y to come
-    Ring<kDeep> ring;  // of the rows to load next
-    const auto load_rows = [&](int c) {
-      const unsigned char *stage = smem + OFF_VG + ring.at * kVG;
-      const auto arr = [&](uint32_t off) { return reinterpret_cast<const float *>(stage + off); };
-      const auto rho = [&](uint32_t off) { return reinterpret_cast<const float *>(smem + ring.at * kTile + off); };
-      const bool ok = wait(BAR_READY + ring.at, ring.parity);
-      vmax = reinterpret_cast<const float *>(smem + OFF_MAXV)[ring.at];
-      gamma_end = arr(OFF_GAMMA)[C - 1];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = row + 8 * i;
-        const bool live = c * C + t < len;  // (the rows after may hold anything)
-        gamma[i] = arr(OFF_GAMMA)[t];
-        beta[i] = live ? arr(OFF_BETA)[t] : 0.f;
-        rho_k[i] = rho(OFF_RHOK)[t];
-        rho_q[i] = rho(OFF_RHOQ)[t];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint32_t u = *reinterpret_cast<const uint32_t *>(stage + (r_at ^ 16 * b) + 1024 * i);
-          v[i][b] = live ? u : 0u;
-        }
-      }
-      ring.next();
-      return ok;
-    };
-    const auto put_y = [&](int c, int k) {  // y of the item's chunk c, the k-th in all
-      wait(BAR_O, k & 1);
-      __syncwarp();
-      tc_fence_after();
-      float o[16];
-      tmem_ld_rows(t_o + lane_off + (16u << 16), o);
-      tmem_ld_wait();
-      const float2 b2 = make_float2(back_o, back_o);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = c * C + row + 8 * i;
-        const long long yo = (base + t) * p.ys + hp + 32 * hf + col;
-        const bool store = t < len && in_bounds(yo + 25, p.y_extent, p.err);
-        const float2 r2 = make_float2(rho_y[i], rho_y[i]);
-        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.y) + yo);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const float2 f = __fmul2_rn(r2, __ffma2_rn(b2, make_float2(o[4 * b + 2 * i], o[4 * b + 2 * i + 1]), hold[i][b]));
-          const __nv_bfloat162 x = __float22bfloat162_rn(f);
-          if (store) dst[4 * b] = *reinterpret_cast<const uint32_t *>(&x);
-        }
-      }
-    };
-    bool ok = true;
-    int k = 0, fulls = 0;  // chunks; items with chunks
-    int seq = 0, hp_next = 0;  // of the next item
-    for (uint32_t i = blockIdx.x; i < n_items + step && ok; i += step) {
-    const int seq_now = seq;
-    hp = hp_next;
-    if (i < n_items) {  // on its way while the item before runs
-      const uint32_t rank = i / per_seq;
-      seq = seq_at(rank);
-      hp_next = 64 * (i - rank * per_seq);
-    }
-    if (i < step) continue;
-    len = seq_len(p.cu, seq_now, p.L);
-    base = seq_base(p.cu, seq_now, p.L);
-    const int nck = (len + C - 1) / C;
-    const long long soff = ((long long)seq_now * p.H * p.P + hp + 32 * hf) * kDState + n;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) S[j] = make_float2(0.f, 0.f);
-    if (p.h0) {
-      const float *src = p.h0 + soff;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) S[j] = make_float2(src[(2 * j) * kDState], src[(2 * j + 1) * kDState]);
-    }
-    m = 0.f;
-    if (p.h0 && nck > 0) {
-      publish_max(2);
-      if (lead) mbar_arrive(BAR(BAR_MAX + hf));
-      ok = wait(BAR_MAX + hf, fulls++ & 1);
-      __syncwarp();
-      m = read_max(2);
-    }
-    sc = state_scale(m);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) S[j] = __fmul2_rn(S[j], make_float2(sc.x, sc.x));
-    if (nck > 0) ok = load_rows(0) && ok;
-    for (int c = 0; c < nck; ++c, ++k) {
-      // S into its operand
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t hv[4], lv[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) split2(S[4 * j + x], hv[x], lv[x]);
-        *reinterpret_cast<uint4 *>(smem + (s_at ^ 16 * j)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-        *reinterpret_cast<uint4 *>(smem + (s_at ^ 16 * (4 + j))) = make_uint4(lv[0], lv[1], lv[2], lv[3]);
-      }
-      fence_proxy_async();
-      tc_fence_before();
-      __syncwarp();
-      if (lead) mbar_arrive(BAR(BAR_SREADY));
-      // while K S^T runs: y of the chunk before, the bound of |S|
-      if (c > 0) put_y(c - 1, k - 1);
-      publish_max(k & 1);
-      const float2 rsc = state_scale(fmaxf(m, vmax));
-      back_o = rsc.y;
-      ok = wait(BAR_D1, k & 1) && ok;
-      __syncwarp();
-      tc_fence_after();
-      {
-        float d[16], e[16];
-        tmem_ld_rows(t_d1 + lane_off, d);
-        tmem_ld_rows(t_d1 + 32 + lane_off, e);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float g = -gamma[i] * sc.y * rho_k[i], bt = beta[i] * rsc.x;
-          const float2 k2 = make_float2(g, g), b2 = make_float2(bt, bt);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int x = 4 * b + 2 * i;
-            const float2 vp = make_float2(__uint_as_float(v[i][b] << 16), __uint_as_float(v[i][b] & 0xffff0000u));
-            const float2 ks = __fadd2_rn(make_float2(d[x], d[x + 1]), make_float2(e[x], e[x + 1]));
-            uint32_t hv, lv;
-            split2(__fmul2_rn(b2, __ffma2_rn(k2, ks, vp)), hv, lv);
-            unsigned char *o = smem + OFF_R + (r_at ^ 16 * b) + 1024 * i;
-            *reinterpret_cast<uint32_t *>(o) = hv;
-            *reinterpret_cast<uint32_t *>(o + 8192) = lv;
-          }
-        }
-        tmem_ld_rows(t_d1 + lane_off + (16u << 16), d);
-        tmem_ld_rows(t_d1 + 32 + lane_off + (16u << 16), e);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float g = gamma[i] * sc.y;
-          rho_y[i] = rho_q[i];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int x = 4 * b + 2 * i;
-            hold[i][b] = __fmul2_rn(make_float2(g, g), __fadd2_rn(make_float2(d[x], d[x + 1]), make_float2(e[x], e[x + 1])));
-          }
-        }
-      }
-      fence_proxy_async();
-      tc_fence_before();
-      __syncwarp();
-      if (lead) mbar_arrive(BAR(BAR_RREADY + hf));
-      // S = gamma_end S + M R, in the next chunk's scale; while the product runs: the next chunk's rows
-      const float decay = gamma_end * sc.y, bound = vmax;
-      if (c + 1 < nck) ok = load_rows(c + 1) && ok;
-      ok = wait(BAR_S + hf, k & 1) && ok;
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      m = fmaf(decay, read_max(k & 1), bound);
-      sc = state_scale(m);
-      const float ge = decay * sc.x, yn = rsc.y * sc.x;
-      const float2 ge2 = make_float2(ge, ge), y2 = make_float2(yn, yn);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) S[i] = __fmul2_rn(S[i], ge2);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float d[16];
-        tmem_ld16(t_s + 16 * x + lane_off, d);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) S[8 * x + i] = __ffma2_rn(y2, make_float2(d[2 * i], d[2 * i + 1]), S[8 * x + i]);
-      }
-    }
-    if (ok && p.h_final && in_bounds(soff + 31 * kDState, p.state_extent, p.err)) {
-      float *dst = p.h_final + soff;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) dst[j * kDState] = sc.y * (j & 1 ? S[j / 2].y : S[j / 2].x);
-    }
-    if (ok && nck > 0) put_y(nck - 1, k - 1);
-    }
   }
 
   tc_fence_before();
