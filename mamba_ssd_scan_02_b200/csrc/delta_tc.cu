@@ -249,10 +249,15 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float (&v)[16]) {
 // and beta |k|^2 <= 2 the transition does not expand a state row s, so over a chunk
 // |s'| <= gamma |s| + 64 * 2 max|V|, and |R| <= 2 (max|V| + |s|).  With m = gamma max|S_old| + max|V| that
 // is |S| <= (sqrt(128) + 128) m < 140 m and |R| < 282 max(m, max|V|): both below 65504 / 128 = 511.
+// Where m is infinite or NaN both are NaN, and so is then every state row: scaled by what is left of such a
+// bound, the rows without one in them would silently lose their bits.
 __device__ __forceinline__ float2 state_scale(float m) {
-  const int e = min(max((int)((__float_as_uint(m) >> 23) & 255u), 8), 254);
-  return make_float2(__uint_as_float((uint32_t)(260 - e) << 23), __uint_as_float((uint32_t)(e - 6) << 23));
+  const int raw = (int)((__float_as_uint(m) >> 23) & 255u), e = min(max(raw, 8), 254);
+  const uint32_t to = (uint32_t)(260 - e) << 23, from = (uint32_t)(e - 6) << 23;
+  return make_float2(__uint_as_float(raw == 255 ? 0x7fffffffu : to), __uint_as_float(raw == 255 ? 0x7fffffffu : from));
 }
+// (fmaxf would drop a NaN)
+__device__ __forceinline__ float max_bound(float a, float b) { return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b))); }
 
 __global__ void __launch_bounds__(kThreads, 1)
     ssd_delta_chunk_kernel(const __grid_constant__ CUtensorMap tm_v, const DeltaPlan p) {
@@ -432,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c > 0) put_y(c - 1, k - 1);
         if (c == nck) break;
         publish_max(k & 1);
-        const float2 rsc = state_scale(fmaxf(m, vmax));
+        const float2 rsc = state_scale(max_bound(m, vmax));
         back_o = rsc.y;
         ok = wait(BAR_D1, k & 1) && ok;
         __syncwarp();

@@ -276,6 +276,39 @@ def test_a_full_machine_gives_equal_bits(cuda_lib, kernel):
         assert torch.equal(y, first[0][cu[i]:cu[i + 1]]) and torch.equal(h[0], first[1][i]), i
 
 
+@pytest.mark.parametrize("kernel", [SIMT, TENSOR])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("name", ["q", "k", "v", "dt", "b"])
+def test_nan_and_infinity_stay_where_they_belong(cuda_lib, name, bad, kernel):
+    """In one token of one head (or group): no y or state is finite where the definition's is not, and outside of
+    that head, and before that token (its chunk, on the tensor cores), nothing changes."""
+    import torch
+    cfg = ref.config(nheads=4, ngroups=2)
+    cu, t = [0, 90, 290], 200  # token 110 of the second sequence
+    d = ref.inputs(cfg, cu[-1], 2, seed=8)
+    clean = run_packed(cuda_lib, cfg, on_gpu(d), cu, True, kernel)
+    at = {"q": 128 + 5, "k": 128 + 5, "v": 2 * 64 + 9, "dt": 2, "b": 2}[name]  # head 2, group 1
+    g = on_gpu(d)
+    g[name][t, at] = bad
+    y, h = run_packed(cuda_lib, cfg, g, cu, True, kernel)
+    torch.cuda.synchronize()
+    assert cuda_lib.get_device_error() == 0
+    heads = [2, 3] if name in ("q", "k") else [2]
+    other = [i for i in range(4) if i not in heads]
+    first = t if kernel == SIMT else cu[1] + 64
+    yh, ch = (x.view(-1, 4, 64) for x in (y, clean[0]))
+    assert torch.equal(yh[:, other], ch[:, other]) and torch.equal(yh[:first], ch[:first])
+    assert torch.equal(h[0], clean[1][0]) and torch.equal(h[1, other], clean[1][1, other])
+    x = {k: ref.values(v).copy() for k, v in d.items()}
+    x[name][t, at] = bad
+    with np.errstate(all="ignore"):
+        wy, wh = ref.prefill(cfg, x, cu, True)
+    assert not np.any(np.isfinite(host(y)) & ~np.isfinite(wy.reshape(host(y).shape)))
+    assert not np.any(np.isfinite(host(h)) & ~np.isfinite(wh))
+    if name == "q":
+        assert torch.equal(h, clean[1])
+
+
 def test_decode_graph(cuda_lib):
     """Captured decode steps over a pool, with the slots changed between replays."""
     import torch
