@@ -496,19 +496,20 @@ def _check_arg(t, name, dtype, device, shape):
 
 
 def _check_dense(t, name, dtype, device, shape):
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     _check_arg(t, name, dtype, device, shape)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows(t, name, dtype, device, shape):
     """(pointer, elements between consecutive rows) of a token tensor [..., width] whose rows are
     evenly spaced: [B, L, width] rows are L * stride apart between batch rows."""
-    _check_arg(t, name, dtype, device, shape)
     st = t.stride()
-    if st[-1] == 1 and shape[-2] > 1 and (len(shape) == 2 or st[0] == shape[1] * st[1] or shape[0] == 1):
+    if t.dtype is dtype and t.shape == shape and t.device == device and st[-1] == 1 and shape[-2] > 1 and (
+            len(shape) == 2 or shape[0] == 1 or st[0] == shape[1] * st[1]):
         return t.data_ptr(), st[-2]  # (most calls)
+    _check_arg(t, name, dtype, device, shape)
     many = [i for i in range(len(shape) - 1) if shape[i] != 1]
     if st[-1] != 1 and shape[-1] > 1 and 0 not in shape:
         raise ValueError(f"{name}: channels must be contiguous")
@@ -564,29 +565,27 @@ def _delta_prefill(cfg, c, cu, nseq, lead, q, k, v, dt, b, A, dt_bias, h0, y, h_
     lib = load()
     H, P, N, G = c.nheads, c.headdim, c.dstate, c.ngroups
     dev, dtype, f32 = q.device, io_dtype(cfg), torch.float32
+    wide, qk, heads, states = (*lead, H * P), (*lead, G * N), (*lead, H), (nseq, H, P, N)
+    rows = (*_rows(q, "q", dtype, dev, qk), *_rows(k, "k", dtype, dev, qk), *_rows(v, "v", dtype, dev, wide),
+            *_rows(dt, "dt", dtype, dev, heads), *_rows(b, "b", dtype, dev, heads),
+            _check_dense(A, "A", f32, dev, (H,)), _check_dense(dt_bias, "dt_bias", f32, dev, (H,)),
+            None if h0 is None else _check_dense(h0, "h0", f32, dev, states))
     made = []
-
-    def new(*shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=dev)
-        made.append(t)
-        return t
-
     if y is None:
-        y = new(*lead, H * P, dtype=dtype)
+        y = v.new_empty(wide)
+        made.append(y)
     if h_final is None and want_state:
-        h_final = new(nseq, H, P, N, dtype=f32)
+        h_final = A.new_empty(states)
+        made.append(h_final)
     if workspace is None:
         n = (lib.ssd_delta_varlen_workspace_size(ctypes.byref(c), cu, nseq) if cu is not None
              else lib.ssd_delta_workspace_size(ctypes.byref(c)))
-        workspace = new(n, dtype=torch.uint8) if n else None
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+            made.append(workspace)
     args = DeltaArgs(
-        *_rows(q, "q", dtype, dev, (*lead, G * N)), *_rows(k, "k", dtype, dev, (*lead, G * N)),
-        *_rows(v, "v", dtype, dev, (*lead, H * P)), *_rows(dt, "dt", dtype, dev, (*lead, H)),
-        *_rows(b, "b", dtype, dev, (*lead, H)), _check_dense(A, "A", f32, dev, (H,)),
-        _check_dense(dt_bias, "dt_bias", f32, dev, (H,)),
-        None if h0 is None else _check_dense(h0, "h0", f32, dev, (nseq, H, P, N)),
-        *_rows(y, "y", dtype, dev, (*lead, H * P)),
-        None if h_final is None else _check_dense(h_final, "h_final", f32, dev, (nseq, H, P, N)),
+        *rows, *_rows(y, "y", dtype, dev, wide),
+        None if h_final is None else _check_dense(h_final, "h_final", f32, dev, states),
         None if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.numel() * workspace.element_size())
     if cu is None:
