@@ -415,11 +415,19 @@ cudaError_t launch_decode(const DeltaPlan &p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+template <int N>
 struct Ints {
-  int v[960];
+  int v[N];
 };
-__global__ void put_ints_kernel(int *dst, const __grid_constant__ Ints src, int n) {
+template <int N>
+__global__ void put_ints_kernel(int *dst, const __grid_constant__ Ints<N> src, int n) {
   for (int i = threadIdx.x; i < n; i += blockDim.x) dst[i] = src.v[i];
+}
+template <int N>
+void put(int *dst, const int *host, int n, cudaStream_t s) {
+  Ints<N> a;
+  for (int i = 0; i < n; ++i) a.v[i] = host[i];
+  put_ints_kernel<N><<<1, 256, 0, s>>>(dst, a, n);
 }
 
 }  // namespace
@@ -431,13 +439,13 @@ cudaError_t launch_delta_decode(const DeltaPlan &p, cudaStream_t s) {
   return p.bf16 ? launch_decode<__nv_bfloat16>(p, s) : launch_decode<float>(p, s);
 }
 
+// Through kernel parameters: a copy from the caller's memory could not be captured without keeping it.  A
+// launch costs more the more parameters it has.
 cudaError_t launch_put_ints(int *dst, const int *host, int n, cudaStream_t s) {
-  Ints a;
-  for (int at = 0; at < n; at += 960) {
-    const int m = n - at < 960 ? n - at : 960;
-    for (int i = 0; i < m; ++i) a.v[i] = host[at + i];
-    put_ints_kernel<<<1, 256, 0, s>>>(dst + at, a, m);
-  }
+  for (; n > 960; n -= 960, dst += 960, host += 960) put<960>(dst, host, 960, s);
+  if (n <= 64) put<64>(dst, host, n, s);
+  else if (n <= 256) put<256>(dst, host, n, s);
+  else put<960>(dst, host, n, s);
   return cudaGetLastError();
 }
 
