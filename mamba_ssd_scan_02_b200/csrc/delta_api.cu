@@ -163,6 +163,7 @@ ssd_status_t run_prefill(const ssd_delta_config_t *c, const ssd_delta_args_t *a,
   const size_t state = (size_t)b.nseq * c->nheads * c->headdim * kDState * sizeof(float);
   if (a->h0 && a->h_final && a->h0 != a->h_final && ranges_overlap(a->h0, state, a->h_final, state))
     return SSD_ERR_INVALID_ARG;
+  if ((long long)b.nseq * c->nheads * (c->headdim / 64) > 1 << 30) return SSD_ERR_UNSUPPORTED;
   const Layout l = layout(c, b);
   if (l.total && (!a->workspace || a->workspace_bytes < l.total || !aligned(a->workspace, kAlign)))
     return SSD_ERR_WORKSPACE;

@@ -10,9 +10,9 @@ namespace ssd {
 // Tokens per chunk of the tensor-core kernel.
 constexpr int kDeltaChunk = 64;
 // One chunk's workspace records, written by the front end and read by the chunk kernel:
-//  tile    per (chunk, group): the fp16 operand image of 64 key rows then 64 query rows, two halves
-//          of 64 columns, each 128 rows x 128 bytes with the 128-byte swizzle; then the row factors
-//          rho_k[64], rho_q[64] (fp32)
+//  tile    per (chunk, group): the fp16 operand image of 64 key and 64 query rows, 16 of each in turn, two
+//          halves of 64 columns, each 128 rows x 128 bytes with the 128-byte swizzle; then the row
+//          factors rho_k[64], rho_q[64] (fp32)
 //  record  per (chunk, head): the operand images of T~^T hi, T~^T lo and A T (64 rows x 128 bytes each,
 //          swizzled); then beta[64], 2^cs[64] and rho_k 2^{cs at the chunk's end - cs}[64] (fp32)
 constexpr long long kDeltaTileBytes = 32768 + 512;

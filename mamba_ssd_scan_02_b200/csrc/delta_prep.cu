@@ -5,8 +5,8 @@
 // row scaled by the power of two that brings its largest element to [1, 2), exact in fp16 down to
 // 2^-17 of it; rho is that power and the norm's factor), K K^T (fp32) and A~ = tril(Q K^T) (fp16).  Then
 // each warp takes heads of its own:
-//   gates  cs = prefix sums of log2(alpha), in fp64 so that differences keep fp32's relative precision
-//          however large the sums
+//   gates  cs = prefix sums of log2(alpha), in fixed point (32 fractional bits), so that their differences are
+//          exact however large the sums
 //   T~     = (I + L~)^-1, L~_ij = beta_i rho_i^2 K_i.K_j (j < i), in fp32: 16 x 16 diagonal blocks by
 //          substitution, joined by block products with tf32 in two parts (22 bits)
 //   A T    2^{cs_t - cs_j} rho_j (A~ T~)_tj, rounded once to fp16
@@ -14,9 +14,14 @@
 //
 // Why apart from the chunk kernel: inside it this part ran in the same SM as the tcgen05 products, which
 // slow mma.sync down threefold and shared-memory loads twofold, and its latency (about 5 us a chunk)
-// bounded every CTA: 650 us for 8192 tokens x 128 heads.  Here it is spread over all chunks, eight
-// independent warps per SM.  The price is 25 KB of workspace per chunk and head, written once and read
-// once.
+// bounded every CTA: 650 us for 8192 tokens x 128 heads, where the two kernels now take 130 and 245.  Here it
+// is spread over all chunks, twelve independent warps per SM (three CTAs; two of them with rows of one
+// pitch: 154 us).  The price is 25 KB of workspace per chunk and head, written once and read once.
+//
+// What bounds it (8192 tokens x 128 heads, 16384 heads' chunks: 130 us): the shared-memory and store pipe, two
+// thirds busy; 43 % of the issue slots are used, 40 % of the DRAM rate.  Its 404 MB of records alone would
+// take 62 us.  As many heads per CTA as share K K^T (16; 8: 166 us where 16 took 154): the K and Q part costs
+// as much as one head.
 #include "common.cuh"
 #include "delta_mma.cuh"
 #include "delta_plan.h"
@@ -584,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
 cudaError_t launch_delta_front(const DeltaPlan &p_in, cudaStream_t s) {
   cudaError_t e = set_smem_attr(ssd_delta_front_kernel, kSmem, s);
   if (e != cudaSuccess) return e;
-  // As many heads per CTA as share its K K^T, but CTAs for every SM: one head per warp where the chunks
-  // and groups alone are few.
+  // As many heads per CTA as share its K K^T, but CTAs for every SM: one head per warp where the chunks and
+  // groups alone are few.
   DeltaPlan p = p_in;
   p.heads_per_cta = p.n_chunks * p.G >= 2 * 148 ? kMaxHeads : kWarps;
   const dim3 grid((unsigned)p.n_chunks, p.G, (p.hpg + p.heads_per_cta - 1) / p.heads_per_cta);

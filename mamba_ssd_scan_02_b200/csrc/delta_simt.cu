@@ -294,7 +294,9 @@ __global__ void __launch_bounds__((kStageWarps + CW) * 32, 1) delta_recurrent_ke
   }
 }
 
-// One token per row, the state in place in a pool.
+// One token per row, the state in place in a pool.  Bound by HBM: the state read and written once; 64 rows of 128
+// heads x 64 x 128: 90 us, 0.91 of a copy's rate.  Four lanes a row and eight loads of 16 bytes in flight per
+// lane; eight lanes: 99 to 100 us, 16: 121.
 template <typename T, int LPR, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32) delta_decode_kernel(const DeltaPlan p) {
   constexpr int R = WARPS * 32 / LPR;   // state rows of this CTA

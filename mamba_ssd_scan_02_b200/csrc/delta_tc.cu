@@ -11,9 +11,10 @@
 //   S' = 2^{cs_C} S + sum_j R_j (rho_j 2^{cs_C - cs_j} M_j)^T,          M = K^T T~          (N x 64)
 //   y_t = 2^{cs_t} S q_t + sum_j 2^{cs_t - cs_j} rho_j (A~ T~)_tj R_j,   A~_ti = q_t.K_i     (i <= t)
 // The inverse, M and A~ T~ know no decay, and nothing of them depends on the state: the chain from chunk
-// to chunk is two dependent products, K S^T (which gives R) and M R.  One CTA carries 64 state rows
-// of one head through the sequence (the rows are independent given K, so a head of 128 rows is two
-// CTAs).
+// to chunk is two dependent products, K S^T (which gives R) and M R.  A CTA carries 64 state rows of one head
+// through a sequence (the rows are independent given K, so a head of 128 rows is two such items), then the next
+// item's: the grid is one CTA per SM, and an item's first loads and M run while the one before ends (64
+// sequences of up to 700 tokens x 128 heads: 715 us with a CTA per item, 610 so).
 //
 // The front end (delta_prep.cu) computes T~ and A T = 2^{cs_t - cs_j} rho_j (A~ T~)_tj.
 //
@@ -27,11 +28,18 @@
 // beside it) is rounded to 11 bits: y is then rounded to bf16's 8.
 //
 // Roles (16 warps, so that a thread may have 128 registers).  Warps 0-7, the chain: S into its operand, R
-// from K S^T, the new S, y.  Their two halves, 32 state rows each, are chains of their own, one
-// product apart, so that the conversions of the one run beside the products of the other.  Warps 8-11 bring M
+// from K S^T, the new S, y.  Their two halves, 32 state rows each, share the products with K S^T and A T R,
+// whose operands they share, and have M R each, so that one converts while the other's runs.  Warps 8-11 bring M
 // (of the chunk after) into its operand.  Warp 12 issues the MMAs of the chains, warp 13 those of M, warp
 // 14 loads, warp 15 loads T and finds the largest |V| of each chunk.  Hand-overs are mbarriers; every
 // wait is bounded: a timeout makes every role leave and latches SSD_ERR_TIMEOUT.
+//
+// What bounds it: the chain.  A chunk takes 1.8 us (8192 tokens x 128 heads: 245 us on 128 SMs): S into fp16 0.25,
+// K S^T 0.5, R 0.3, M R 0.4 (the next rows load meanwhile), the new S 0.25; the tensor pipe is 46 % busy, the issue
+// slots 60 %, DRAM 33 %.  A product per half for K S^T (the halves half a chunk apart, one issuer each or one
+// for both) took 255 to 260 us where the shared one takes 232: the K and Q operand is read twice.  The code
+// is kept small (loops rolled, one place per inlined part): sixteen warps in six roles share an
+// instruction cache, and 10 KB more of it cost 5 to 10 %.
 #include <cudaTypedefs.h>
 #include <algorithm>
 

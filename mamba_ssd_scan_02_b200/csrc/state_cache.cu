@@ -8,7 +8,9 @@
 //
 // Bound by HBM: 4 bytes read and 33/32 written per element (store), the reverse (load).  A warp
 // takes 128 elements (four blocks) per step: eight lanes per block with 16 bytes each, so every
-// access is a full line, and UNROLL steps are in flight.
+// access is a full line, and kUnroll consecutive steps are in flight, whose scales are a full sector.
+// 64 states of 128 heads x 64 x 128: store 55.6 us (65 with the scales written step by step), load 54 us,
+// 0.93 and 0.96 of a copy's rate.
 #include <cuda_fp8.h>
 
 #include "common.cuh"

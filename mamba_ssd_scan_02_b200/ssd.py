@@ -10,6 +10,9 @@ Tensor conventions (all on one CUDA device, channels contiguous):
   A, D, dt_bias [H] float32, conv_w [conv_dim, W], conv_b [conv_dim], norm_w [d_inner],
   h0 / h_final [B, H, 64, 128] float32, conv caches [B, W, conv_dim], y [B, L, d_inner].
 bf16 io uses torch.bfloat16; the fp32 io path uses torch.float32.
+
+The gated delta rule (delta_*) takes q, k [B, L, G*N], v [B, L, H*P] and the raw gates dt, b
+[B, L, H]; the state cache (state_*) keeps fp32 states of either layer in 8 bits.
 """
 from __future__ import annotations
 
