@@ -76,7 +76,7 @@ __global__ void __launch_bounds__((kStageWarps + CW) * 32, 1) delta_recurrent_ke
   const int g = h / p.hpg;
   const int len = seq_len(p.cu, seq, p.L);
   const long long base = seq_base(p.cu, seq, p.L);
-  const float A = p.A[h], bias = p.dt_bias[h];
+  const float A = len > 0 ? p.A[h] : 0.f, bias = len > 0 ? p.dt_bias[h] : 0.f;  // (null where no tokens are)
   const T *q = static_cast<const T *>(p.q) + base * p.qs + g * kDState + 4 * lane;
   const T *k = static_cast<const T *>(p.k) + base * p.ks + g * kDState + 4 * lane;
   const T *v = static_cast<const T *>(p.v) + base * p.vs + h * p.P + row0;

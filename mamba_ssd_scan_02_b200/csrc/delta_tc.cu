@@ -120,15 +120,15 @@ constexpr uint32_t IDESC_M = idesc_f16(128, 128, true, false, kFmtF16);   // K^T
 constexpr uint32_t IDESC_S = idesc_f16(128, 32, false, true, kFmtF16);    // M (TMEM) . R of a half
 constexpr uint32_t IDESC_O = idesc_f16(128, 64, false, true, kFmtF16);    // A T . R_hi of both halves
 
-// A bounded wait.  A try suspends the warp for a while in hardware; after every 256 the abort flag is
-// looked at, and after 2^17 times that (about a second) the flag is set to 2.  In one piece of
+// A bounded wait.  A try suspends the warp for up to 7800 clocks (4 us); after every 256 the abort flag is
+// looked at, and after 2^11 times that (two seconds) the flag is set to 2.  In one piece of
 // assembly, because a warp that waits should issue little (about half of them wait at any time), and
 // because every wait of every role sits in the instruction cache.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint32_t abort) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n, m, f;\n\t"
-      "mov.u32 m, 131072;\n"
+      "mov.u32 m, 2048;\n"
       "OUTER_%=:\n\t"
       "mov.u32 n, 256;\n"
       "TRY_%=:\n\t"

@@ -249,6 +249,27 @@ def test_streams_graphs_and_repeats(cuda_lib, kernel):
     assert none is None and torch.equal(y0, y2)
 
 
+@pytest.mark.parametrize("packed", [False, True])
+def test_no_tokens_need_only_the_states(cuda_lib, packed):
+    """With no token at all, every pointer but the states' (and a packed call's workspace) may be null."""
+    import ctypes
+    import torch
+    cfg = ref.config(nheads=4)
+    h0 = torch.randn(3, 4, 64, 128, device="cuda")
+    out = torch.zeros_like(h0)
+    ws = torch.empty(4096, dtype=torch.uint8, device="cuda")
+    args = cuda_lib.DeltaArgs(h0=h0.data_ptr(), h_final=out.data_ptr(), workspace=ws.data_ptr(), workspace_bytes=4096)
+    lib, stream = cuda_lib.load(), torch.cuda.current_stream().cuda_stream
+    if packed:
+        c = cuda_lib.make_delta_config(cfg, 1, 0)
+        status = lib.ssd_delta_prefill_varlen(ctypes.byref(c), ctypes.byref(args), (ctypes.c_int * 4)(0, 0, 0, 0), 3, stream)
+    else:
+        c = cuda_lib.make_delta_config(cfg, 3, 0)
+        status = lib.ssd_delta_prefill(ctypes.byref(c), ctypes.byref(args), stream)
+    torch.cuda.synchronize()
+    assert status == 0 and torch.equal(out, h0) and cuda_lib.get_device_error() == 0
+
+
 @pytest.mark.parametrize("kernel", [SIMT, TENSOR])
 def test_a_full_machine_gives_equal_bits(cuda_lib, kernel):
     """Many sequences at once, on every SM: the same bits whatever the workspace held and whatever the L2
