@@ -587,7 +587,8 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
 }  // namespace
 
 cudaError_t launch_delta_front(const DeltaPlan &p_in, cudaStream_t s) {
-  cudaError_t e = set_smem_attr(ssd_delta_front_kernel, kSmem, s);
+  // (also while the stream is captured: it may be the process's first call)
+  cudaError_t e = cudaFuncSetAttribute(ssd_delta_front_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   // As many heads per CTA as share its K K^T, but CTAs for every SM: one head per warp where the chunks and
   // groups alone are few.

@@ -762,7 +762,8 @@ cudaError_t launch_delta_chunks(const DeltaPlan &p, cudaStream_t s) {
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  cudaError_t e = set_smem_attr(ssd_delta_chunk_kernel, kSmem, s);
+  // (also while the stream is captured: it may be the process's first call)
+  cudaError_t e = cudaFuncSetAttribute(ssd_delta_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   // a programmatic dependent of the front end: its set-up and first loads of V overlap the front
   // end's tail

@@ -249,6 +249,44 @@ def test_streams_graphs_and_repeats(cuda_lib, kernel):
     assert none is None and torch.equal(y0, y2)
 
 
+FIRST_CALL = """
+import torch
+from mamba_ssd_scan_02_b200 import ssd
+cfg = dict(nheads=4, headdim=64, dstate=128, ngroups=2, dtype="bf16")
+z = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+t = [z(200, 256), z(200, 256), z(200, 256), z(200, 4), z(200, 4), -torch.rand(4, device="cuda"), torch.zeros(4, device="cuda")]
+step = [x[:2].clone() for x in t[:5]] + t[5:]
+
+def calls(kernel):
+    y, h = ssd.delta_prefill_varlen(cfg, [0, 120, 200], *t, kernel=kernel)
+    cache, scales = ssd.state_cache(2, (4, 64, 128))
+    ssd.state_store(h, cache, scales)
+    back = ssd.state_load(cache, scales, torch.empty_like(h))
+    y_t = ssd.delta_decode_step(cfg, *step, back)
+    return y, h, back, y_t
+
+torch.cuda.synchronize()
+for kernel in (2, 1):
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls(kernel)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, calls(kernel))), kernel
+assert ssd.get_device_error() == 0
+"""
+
+
+def test_first_calls_of_a_process_in_a_capture(cuda_lib):
+    """A prompt, its states through the cache, a token: captured before anything else has run."""
+    import subprocess
+    import sys
+    from pathlib import Path
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=Path(__file__).resolve().parent.parent, capture_output=True,
+                       text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 @pytest.mark.parametrize("packed", [False, True])
 def test_no_tokens_need_only_the_states(cuda_lib, packed):
     """With no token at all, every pointer but the states' (and a packed call's workspace) may be null."""
