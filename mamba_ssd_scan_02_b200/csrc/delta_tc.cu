@@ -79,7 +79,8 @@ constexpr uint32_t OFF_VG = OFF_AT + 2 * kAT;
 constexpr uint32_t OFF_SB = OFF_VG + kDeep * kVG;  // S operands of the halves: [n][32 p hi, 32 p lo], 128 rows each
 constexpr uint32_t OFF_R = OFF_SB + 2 * kHalf;    // R operands: [token][32 p of each half], 64 rows of hi, 64 of lo
 constexpr uint32_t OFF_MAXS = OFF_R + 2 * 8192;      // largest |S| per chain warp: two chunks, an item's first
-constexpr uint32_t OFF_MAXV = OFF_MAXS + 128;     // bound of what the chunk adds, per place in the ring
+constexpr uint32_t OFF_SCALE = OFF_MAXS + 128;    // per half and chunk parity: the scales of S and R, backwards
+constexpr uint32_t OFF_MAXV = OFF_SCALE + 32;     // bound of what the chunk adds, per place in the ring
 constexpr uint32_t OFF_BAR = OFF_MAXV + 64;
 // A barrier that can complete again before every waiter has seen the phase before has one copy per
 // buffer, so that a parity test never sees two phases at once.
@@ -93,7 +94,7 @@ enum {
   BAR_M = BAR_AT + 2,              // [2] M done
   BAR_MREADY = BAR_M + 2,          // [2] M operand in tensor memory (4 warps)
   BAR_SREADY = BAR_MREADY + 2,     // S operand written (8 warps)
-  BAR_RREADY = BAR_SREADY + 1,     // [2 halves] R operand written, D1 read (4 warps)
+  BAR_RREADY = BAR_SREADY + 1,     // [2 halves] R operand written, D1 read (4 chain warps, 4 y warps)
   BAR_D1 = BAR_RREADY + 2,         // K S^T, Q S^T done
   BAR_S = BAR_D1 + 1,              // [2 halves] M R done
   BAR_O = BAR_S + 2,               // A T R done
@@ -170,7 +171,7 @@ struct Ring {
 __device__ __forceinline__ uint32_t op_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | (lbo >> 4) << 16; }
 constexpr uint32_t kOpHi = 1024 >> 4 | 1u << 14 | 2u << 29;
 __device__ __forceinline__ constexpr uint32_t kstep(int j) { return ((j >> 2) * kHalf + (j & 3) * 32) >> 4; }
-__device__ __forceinline__ constexpr uint32_t tstep(int j) { return (j >> 1) * 32 + (j & 1) * 8; }
+__device__ __forceinline__ constexpr uint32_t tstep(int j) { return 16 * j; }
 
 // The issuing warps run converged and elect a lane per instruction, and what the descriptors come from is
 // broadcast with shuffles: the compiler then knows it to be uniform and keeps the descriptors in uniform
@@ -224,7 +225,7 @@ __device__ __forceinline__ void issue_S(uint32_t m, uint32_t r, int half, uint32
   const uint32_t hi = op_lo(r, 8192) + 4 * half, lo = op_lo(r + 8192, 8192) + 4 * half;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    mma_ts<IDESC_S>(d, m + tstep(j) + 16, hi + 128 * j, j > 0);
+    mma_ts<IDESC_S>(d, m + tstep(j) + 8, hi + 128 * j, j > 0);
     mma_ts<IDESC_S>(d, m + tstep(j), lo + 128 * j, true);
   }
 #pragma unroll
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(BAR(i), i == BAR_SREADY ? 8 : i >= BAR_MREADY && i < BAR_D1 || i >= BAR_MAX ? 4 : 1);
+      mbar_init(BAR(i), i >= BAR_SREADY && i < BAR_D1 ? 8 : i >= BAR_MREADY && i < BAR_SREADY || i >= BAR_MAX ? 4 : 1);
     misc[1] = misc[2] = 0;
     fence_mbar_init();
   }
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // at r_at ^ 16 b
     const uint32_t s_at = OFF_SB + hf * kHalf + swz(n, 0), r_at = swz(row, 4 * hf) + 2 * col;
     uint32_t *max_s = reinterpret_cast<uint32_t *>(smem + OFF_MAXS) + 12 * hf;
-    const uint32_t t_d1 = tmem + TM_D1 + 64 * hf, t_s = tmem + TM_S + 32 * hf, t_o = tmem + TM_O + 32 * hf;
+    const uint32_t t_d1 = tmem + TM_D1 + 64 * hf, t_s = tmem + TM_S + 32 * hf;
     float2 S[16];  // the state, times sc.x
     int len = 0;             // of the item: tokens, the first of them's row, and h P + the first state row
     long long base = 0;
@@ -335,14 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m;    // bounds the state as described at state_scale
     float2 sc;
     uint32_t v[2][4];                  // the chunk's V, pairs
-    float2 hold[2][4];                 // 2^cs Q S^T of the chunk whose y is still to come
-    float gamma[2], beta[2], rho_k[2], rho_q[2], gamma_end = 0.f, vmax = 0.f;  // of the chunk
-    float back_o = 0.f, rho_y[2];      // of the y to come
+    float gamma[2], beta[2], rho_k[2], gamma_end = 0.f, vmax = 0.f;  // of the chunk
     Ring<kDeep> ring;  // of the rows to load next
     const auto load_rows = [&](int c) {
       const unsigned char *stage = smem + OFF_VG + ring.at * kVG;
       const auto arr = [&](uint32_t off) { return reinterpret_cast<const float *>(stage + off); };
-      const auto rho = [&](uint32_t off) { return reinterpret_cast<const float *>(smem + ring.at * kTile + off); };
       const bool ok = wait(BAR_READY + ring.at, ring.parity);
       vmax = reinterpret_cast<const float *>(smem + OFF_MAXV)[ring.at];
       gamma_end = arr(OFF_GAMMA)[C - 1];
@@ -352,8 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool live = c * C + t < len;  // (the rows after may hold anything)
         gamma[i] = arr(OFF_GAMMA)[t];
         beta[i] = live ? arr(OFF_BETA)[t] : 0.f;
-        rho_k[i] = rho(OFF_RHOK)[t];
-        rho_q[i] = rho(OFF_RHOQ)[t];
+        rho_k[i] = reinterpret_cast<const float *>(smem + ring.at * kTile + OFF_RHOK)[t];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const uint32_t u = *reinterpret_cast<const uint32_t *>(stage + (r_at ^ 16 * b) + 1024 * i);
@@ -362,29 +359,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ring.next();
       return ok;
-    };
-    const auto put_y = [&](int c, int k) {  // y of the item's chunk c, the k-th in all
-      wait(BAR_O, k & 1);
-      __syncwarp();
-      tc_fence_after();
-      float o[16];
-      tmem_ld_rows(t_o + lane_off + (16u << 16), o);
-      tmem_ld_wait();
-      const float2 b2 = make_float2(back_o, back_o);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = c * C + row + 8 * i;
-        const long long yo = (base + t) * p.ys + hp + 32 * hf + col;
-        const bool store = t < len && in_bounds(yo + 25, p.y_extent, p.err);
-        const float2 r2 = make_float2(rho_y[i], rho_y[i]);
-        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.y) + yo);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const float2 f = __fmul2_rn(r2, __ffma2_rn(b2, make_float2(o[4 * b + 2 * i], o[4 * b + 2 * i + 1]), hold[i][b]));
-          const __nv_bfloat162 x = __float22bfloat162_rn(f);
-          if (store) dst[4 * b] = *reinterpret_cast<const uint32_t *>(&x);
-        }
-      }
     };
     bool ok = true;
     int k = 0, fulls = 0;  // chunks; items with chunks
@@ -441,12 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) dst[j * kDState] = sc.y * (j & 1 ? S[j / 2].y : S[j / 2].x);
         }
-        // while K S^T runs: y of the chunk before, the bound of |S|
-        if (c > 0) put_y(c - 1, k - 1);
         if (c == nck) break;
+        // while K S^T runs: the bound of |S|
         publish_max(k & 1);
         const float2 rsc = state_scale(max_bound(m, vmax));
-        back_o = rsc.y;
+        if (q4 == 0 && lead) reinterpret_cast<float2 *>(smem + OFF_SCALE)[2 * hf + (k & 1)] = make_float2(sc.y, rsc.y);
         ok = wait(BAR_D1, k & 1) && ok;
         __syncwarp();
         tc_fence_after();
@@ -469,19 +442,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               unsigned char *o = smem + OFF_R + (r_at ^ 16 * b) + 1024 * i;
               *reinterpret_cast<uint32_t *>(o) = hv;
               *reinterpret_cast<uint32_t *>(o + 8192) = lv;
-            }
-          }
-          tmem_ld_rows(t_d1 + lane_off + (16u << 16), d);
-          tmem_ld_rows(t_d1 + 32 + lane_off + (16u << 16), e);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float g = gamma[i] * sc.y;
-            rho_y[i] = rho_q[i];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const int x = 4 * b + 2 * i;
-              hold[i][b] = __fmul2_rn(make_float2(g, g), __fadd2_rn(make_float2(d[x], d[x + 1]), make_float2(e[x], e[x + 1])));
             }
           }
         }
@@ -514,41 +474,119 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------------ M, its columns times
-    // rho_j 2^{cs_C - cs_j}, into its operand
-    Ring<kDeep> r;
+    // rho_j 2^{cs_C - cs_j}, into its operand, a chunk ahead; y
+    const int row = 16 * q4 + (lane >> 2), col = 2 * (lane & 3);  // tokens and columns as the chains'
+    uint32_t total = 0;  // chunks of all items
+    for (uint32_t i = blockIdx.x + lane * step; i < n_items; i += 32 * step) total += chunks_of(i);
+    total = __reduce_add_sync(0xffffffffu, total);
+    Ring<kDeep> r, ry;  // of the chunk whose M is next; of the one whose y is
     bool ok = true;
-    int k = 0;
-    for (uint32_t i = blockIdx.x, nck = 0, next; i < n_items + step && ok; i += step, nck = next) {
-      next = chunks_of(i);
-      for (uint32_t c = 0; c < nck; ++c, ++k, r.next()) {
-        ok = wait(BAR_VG + r.at, r.parity);  // the factors
-        ok = wait2(BAR_M, k) && ok;
+    const auto convert = [&](uint32_t k) {
+      ok = wait(BAR_VG + r.at, r.parity) && ok;  // the factors
+      ok = wait2(BAR_M, k) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      const float4 *f = reinterpret_cast<const float4 *>(smem + OFF_VG + r.at * kVG + OFF_END);
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {  // 16 tokens
+        const uint32_t at = tmem + TM_M + 128 * (k & 1) + lane_off;
+        float m[16], e[16];
+        uint32_t hv[8], lv[8];
+        tmem_ld16(at + 16 * b, m);
+        tmem_ld16(at + 64 + 16 * b, e);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 x = f[4 * b + j];
+          const auto sum = [&](int i) { return __fadd2_rn(make_float2(m[i], m[i + 1]), make_float2(e[i], e[i + 1])); };
+          split2(__fmul2_rn(sum(4 * j), make_float2(x.x, x.y)), hv[2 * j], lv[2 * j]);
+          split2(__fmul2_rn(sum(4 * j + 2), make_float2(x.z, x.w)), hv[2 * j + 1], lv[2 * j + 1]);
+        }
+        tmem_st8(at + 16 * b, hv);
+        tmem_st8(at + 16 * b + 8, lv);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lead) mbar_arrive(BAR(BAR_MREADY + (k & 1)));
+      r.next();
+    };
+    uint32_t k = 0;
+    if (total > 0) convert(0);
+    int seq = 0, hp_next = 0;  // of the next item
+    for (uint32_t i = blockIdx.x; i < n_items + step && ok; i += step) {
+      const int seq_now = seq, hp = hp_next;
+      if (i < n_items) {  // on its way while the item before runs
+        const uint32_t rank = i / per_seq;
+        seq = seq_at(rank);
+        hp_next = 64 * (i - rank * per_seq);
+      }
+      if (i < step) continue;
+      const int len = seq_len(p.cu, seq_now, p.L), nck = (len + C - 1) / C;
+      const long long base = seq_base(p.cu, seq_now, p.L);
+      for (int c = 0; c < nck; ++c, ++k) {
+        // Q S^T, out of the next chunk's way
+        ok = wait(BAR_D1, k & 1) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const float4 *f = reinterpret_cast<const float4 *>(smem + OFF_VG + r.at * kVG + OFF_END);
-#pragma unroll 1
-        for (int b = 0; b < 2; ++b) {
-          const uint32_t at = tmem + TM_M + 128 * (k & 1) + 32 * b + lane_off;
-          float m[32], e[32];
-          uint32_t hv[16], lv[16];
-          tmem_ld32(at, m);
-          tmem_ld32(at + 64, e);
+        float2 hold[2][2][4];  // [half][token]
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          float d[16], e[16];
+          tmem_ld_rows(tmem + TM_D1 + 64 * hf + lane_off + (16u << 16), d);
+          tmem_ld_rows(tmem + TM_D1 + 64 * hf + 32 + lane_off + (16u << 16), e);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 x = f[8 * b + j];
-            const auto sum = [&](int i) { return __fadd2_rn(make_float2(m[i], m[i + 1]), make_float2(e[i], e[i + 1])); };
-            split2(__fmul2_rn(sum(4 * j), make_float2(x.x, x.y)), hv[2 * j], lv[2 * j]);
-            split2(__fmul2_rn(sum(4 * j + 2), make_float2(x.z, x.w)), hv[2 * j + 1], lv[2 * j + 1]);
-          }
-          tmem_st16(at, hv);
-          tmem_st16(at + 16, lv);
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const int x = 4 * b + 2 * t;
+              hold[hf][t][b] = __fadd2_rn(make_float2(d[x], d[x + 1]), make_float2(e[x], e[x + 1]));
+            }
         }
-        tmem_st_wait();
+        ok = wait(BAR_TILE + ry.at, ry.parity) && ok;  // (done: what it loaded is read here)
+        float gamma[2], rho[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          gamma[t] = reinterpret_cast<const float *>(smem + OFF_VG + ry.at * kVG + OFF_GAMMA)[row + 8 * t];
+          rho[t] = reinterpret_cast<const float *>(smem + ry.at * kTile + OFF_RHOQ)[row + 8 * t];
+        }
+        ry.next();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(BAR_MREADY + (k & 1)));
+        if (lead) {
+          mbar_arrive(BAR(BAR_RREADY));
+          mbar_arrive(BAR(BAR_RREADY + 1));
+        }
+        if (k + 1 < total) convert(k + 1);
+        ok = wait(BAR_O, k & 1) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float2 sc = reinterpret_cast<const float2 *>(smem + OFF_SCALE)[2 * hf + (k & 1)];
+          float o[16];
+          tmem_ld_rows(tmem + TM_O + 32 * hf + lane_off + (16u << 16), o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int token = c * C + row + 8 * t;
+            const long long yo = (base + token) * p.ys + hp + 32 * hf + col;
+            const bool store = token < len && in_bounds(yo + 25, p.y_extent, p.err);
+            const float g = gamma[t] * sc.x;
+            const float2 r2 = make_float2(rho[t], rho[t]), b2 = make_float2(sc.y, sc.y), g2 = make_float2(g, g);
+            uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.y) + yo);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const float2 w = __ffma2_rn(b2, make_float2(o[4 * b + 2 * t], o[4 * b + 2 * t + 1]), __fmul2_rn(g2, hold[hf][t][b]));
+              const __nv_bfloat162 x = __float22bfloat162_rn(__fmul2_rn(r2, w));
+              if (store) dst[4 * b] = *reinterpret_cast<const uint32_t *>(&x);
+            }
+          }
+        }
+        tc_fence_before();
       }
     }
   } else if (warp == 12) {
