@@ -94,13 +94,14 @@ enum {
   BAR_M = BAR_AT + 2,              // [2] M done
   BAR_MREADY = BAR_M + 2,          // [2] M operand in tensor memory (4 warps)
   BAR_SREADY = BAR_MREADY + 2,     // S operand written (8 warps)
-  BAR_RREADY = BAR_SREADY + 1,     // [2 halves] R operand written, D1 read (4 chain warps, 4 y warps)
+  BAR_RREADY = BAR_SREADY + 1,     // [2 halves] R operand written, K S^T read (4 warps)
   BAR_D1 = BAR_RREADY + 2,         // K S^T, Q S^T done
   BAR_S = BAR_D1 + 1,              // [2 halves] M R done
   BAR_O = BAR_S + 2,               // A T R done
   BAR_DONE = BAR_O + 1,            // [2] nothing of an issuer's left in flight
   BAR_MAX = BAR_DONE + 2,          // [2 halves] the bounds of an item's first state written (4 warps)
-  kNumBars = BAR_MAX + 2
+  BAR_QREAD = BAR_MAX + 2,         // Q S^T read, and the y before it done (4 warps)
+  kNumBars = BAR_QREAD + 1
 };
 constexpr uint32_t OFF_MISC = OFF_BAR + 8 * 32;   // [0] TMEM base, [1] abort flag, [2] the same for the last waits
 constexpr uint32_t kSmem = OFF_MISC + 16 + 1024;  // room to align the base to 1024 bytes
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(BAR(i), i >= BAR_SREADY && i < BAR_D1 ? 8 : i >= BAR_MREADY && i < BAR_SREADY || i >= BAR_MAX ? 4 : 1);
+      mbar_init(BAR(i), i == BAR_SREADY ? 8 : i >= BAR_MREADY && i < BAR_D1 || i >= BAR_MAX ? 4 : 1);
     misc[1] = misc[2] = 0;
     fence_mbar_init();
   }
@@ -419,10 +420,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // while K S^T runs: the bound of |S|
         publish_max(k & 1);
         const float2 rsc = state_scale(max_bound(m, vmax));
-        if (q4 == 0 && lead) reinterpret_cast<float2 *>(smem + OFF_SCALE)[2 * hf + (k & 1)] = make_float2(sc.y, rsc.y);
         ok = wait(BAR_D1, k & 1) && ok;
         __syncwarp();
         tc_fence_after();
+        // (for y; the place is free: the product was issued after the y of two chunks before)
+        if (q4 == 0 && lead) reinterpret_cast<float2 *>(smem + OFF_SCALE)[2 * hf + (k & 1)] = make_float2(sc.y, rsc.y);
         {
           float d[16], e[16];
           tmem_ld_rows(t_d1 + lane_off, d);
@@ -555,10 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ry.next();
         tc_fence_before();
         __syncwarp();
-        if (lead) {
-          mbar_arrive(BAR(BAR_RREADY));
-          mbar_arrive(BAR(BAR_RREADY + 1));
-        }
+        if (lead) mbar_arrive(BAR(BAR_QREAD));
         if (k + 1 < total) convert(k + 1);
         ok = wait(BAR_O, k & 1) && ok;
         ok = __all_sync(0xffffffffu, ok);
@@ -611,6 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           commit(BAR(BAR_S + half));
         }
         ok = wait2(BAR_AT, k) && ok;
+        ok = wait(BAR_QREAD, k & 1) && ok;
+        tc_fence_after();
         issue_O(sb + OFF_AT + (k & 1) * 2048, sb + OFF_R, tmem + TM_O);
         commit(BAR(BAR_O));
         commit(BAR(BAR_EMPTY + r.at));
