@@ -28,18 +28,21 @@
 // beside it) is rounded to 11 bits: y is then rounded to bf16's 8.
 //
 // Roles (16 warps, so that a thread may have 128 registers).  Warps 0-7, the chain: S into its operand, R
-// from K S^T, the new S, y.  Their two halves, 32 state rows each, share the products with K S^T and A T R,
-// whose operands they share, and have M R each, so that one converts while the other's runs.  Warps 8-11 bring M
-// (of the chunk after) into its operand.  Warp 12 issues the MMAs of the chains, warp 13 those of M, warp
-// 14 loads, warp 15 loads T and finds the largest |V| of each chunk.  Hand-overs are mbarriers; every
-// wait is bounded: a timeout makes every role leave and latches SSD_ERR_TIMEOUT.
+// from K S^T, the new S.  Their two halves, 32 state rows each, share the product with K, whose operand is
+// read once for both, and have M R each, so that one converts while the other's runs.  Warps 8-11 bring M (of
+// the chunk after) into its operand and make y from Q S^T and A T R, neither in the chain's way.  Warp 12
+// issues the MMAs of the chains, warp 13 those of M, warp 14 loads, warp 15 loads T and finds the largest |V|
+// of each chunk.  Hand-overs are mbarriers; every wait is bounded: a timeout makes every role leave and
+// latches SSD_ERR_TIMEOUT.
 //
-// What bounds it: the chain.  A chunk takes 1.8 us (8192 tokens x 128 heads: 245 us on 128 SMs): S into fp16 0.25,
-// K S^T 0.5, R 0.3, M R 0.4 (the next rows load meanwhile), the new S 0.25; the tensor pipe is 46 % busy, the issue
-// slots 60 %, DRAM 33 %.  A product per half for K S^T (the halves half a chunk apart, one issuer each or one
-// for both) took 255 to 260 us where the shared one takes 232: the K and Q operand is read twice.  The code
-// is kept small (loops rolled, one place per inlined part): sixteen warps in six roles share an
-// instruction cache, and 10 KB more of it cost 5 to 10 %.
+// What bounds it: the chain.  A chunk takes 1.7 us (8192 tokens x 128 heads: 217 us on 128 SMs; 245 at the clocks
+// that a second of such calls leaves): S into fp16 0.25 (the halves one after the other 0.5), K S^T 0.4, R 0.25,
+// M R 0.35 (the next rows load meanwhile), the new S 0.2; the tensor pipe is 53 % busy, the issue slots 56 %, DRAM
+// 36 %.  Measured against it, at the stage each was tried: y by the chain's warps 246 us where this took 226;
+// M R waiting for the readers of Q S^T 226 : 213; one M R for both halves 246 : 226; a product per half for
+// K S^T (the halves half a chunk apart, one issuer each or one for both) 255 to 260 : 232, since the K and Q
+// operand is then read twice.  The code is kept small (loops rolled, one place per inlined part): sixteen
+// warps in six roles share an instruction cache, and 10 KB more of it cost 5 to 10 %.
 #include <cudaTypedefs.h>
 #include <algorithm>
 
@@ -109,12 +112,12 @@ static_assert(kNumBars <= 32 && kSmem <= 232448, "shared memory");
 static_assert(OFF_SB % 1024 == 0 && OFF_R % 1024 == 0 && OFF_T % 1024 == 0 && OFF_VG % 1024 == 0, "swizzle alignment");
 
 // TMEM columns.  M: twice 64 columns of the product with T's hi and 64 of that with its lo; the M operand
-// replaces the former (tokens 32 b .. 32 b + 31 in the columns 32 b .. , hi first, lo 16 columns on).  Of every 32
-// lanes of D1 the first 16 are K rows, the others the Q rows of the same tokens, as are the rows of A T R (the other
-// lanes of it are never used): each of the four warps that can read a quarter of the lanes then has as much to
-// convert (with the K rows in lanes 0-63, two of them had all of R to convert, on two of the four schedulers; 240
-// us where this takes 232, 8192 tokens x 128 heads).  D1 has
-// per half 32 columns of the products with hi, 32 of those with lo, S and O 32 columns.
+// replaces the former (tokens 16 j .. in the columns 16 j .. , hi first, lo 8 columns on).  Of every 32 lanes of
+// D1 the first 16 are K rows, the others the Q rows of the same tokens, as are the rows of A T R (the other
+// lanes of it are never used): each of the four warps that can read a quarter of the lanes then has as
+// much to convert (with the K rows in lanes 0-63, two of them had all of R to convert, on two of the four
+// schedulers: 240 us where this took 232, 8192 tokens x 128 heads).  D1 has per half 32 columns of the products
+// with hi, 32 of those with lo, S and O 32 columns.
 constexpr uint32_t TM_M = 0, TM_D1 = 256, TM_S = 384, TM_O = 448, TM_COLS = 512;
 
 constexpr uint32_t IDESC_D1 = idesc_f16(128, 128, false, true, kFmtF16);  // [K; Q] . S of both halves
