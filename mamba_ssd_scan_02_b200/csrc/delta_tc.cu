@@ -575,17 +575,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int token = c * C + row + 8 * t;
-            const long long yo = (base + token) * p.ys + hp + 32 * hf + col;
-            const bool store = token < len && in_bounds(yo + 25, p.y_extent, p.err);
             const float g = gamma[t] * sc.x;
             const float2 r2 = make_float2(rho[t], rho[t]), b2 = make_float2(sc.y, sc.y), g2 = make_float2(g, g);
-            uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.y) + yo);
+            uint32_t u[4];
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
               const float2 w = __ffma2_rn(b2, make_float2(o[4 * b + 2 * t], o[4 * b + 2 * t + 1]), __fmul2_rn(g2, hold[hf][t][b]));
               const __nv_bfloat162 x = __float22bfloat162_rn(__fmul2_rn(r2, w));
-              if (store) dst[4 * b] = *reinterpret_cast<const uint32_t *>(&x);
+              u[b] = *reinterpret_cast<const uint32_t *>(&x);
             }
+            // a row's four lanes exchange, so that lane l % 4 has the columns 8 (l % 4) ..: 16 bytes to store
+            const bool odd = lane & 1, up = lane & 2;
+            uint32_t e0 = __shfl_xor_sync(0xffffffffu, odd ? u[0] : u[1], 1), e1 = __shfl_xor_sync(0xffffffffu, odd ? u[2] : u[3], 1);
+            const uint32_t a0 = odd ? e0 : u[0], a1 = odd ? u[1] : e0, c0 = odd ? e1 : u[2], c1 = odd ? u[3] : e1;
+            e0 = __shfl_xor_sync(0xffffffffu, up ? a0 : c0, 2);
+            e1 = __shfl_xor_sync(0xffffffffu, up ? a1 : c1, 2);
+            const long long yo = (base + token) * p.ys + hp + 32 * hf + 4 * col;
+            if (token < len && in_bounds(yo + 7, p.y_extent, p.err))
+              *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.y) + yo) =
+                  up ? make_uint4(e0, e1, c0, c1) : make_uint4(a0, a1, e0, e1);
           }
         }
         tc_fence_before();
