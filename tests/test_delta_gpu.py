@@ -287,6 +287,49 @@ def test_first_calls_of_a_process_in_a_capture(cuda_lib):
     assert r.returncode == 0, r.stderr[-2000:]
 
 
+def test_two_calls_at_once(cuda_lib):
+    """Chunked kernels and the recurrence on two streams at the same time: the bits of each alone."""
+    import torch
+    cfg = ref.config(nheads=32, ngroups=4)
+    g = on_gpu(ref.inputs(cfg, 1500, 1, seed=12))
+    alone = {k: run_packed(cuda_lib, cfg, g, [0, 1500], True, k) for k in (SIMT, TENSOR)}
+    streams = {k: torch.cuda.Stream() for k in alone}
+    for s in streams.values():
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(4):
+        for k, s in streams.items():
+            got.append((k, run_packed(cuda_lib, cfg, g, [0, 1500], True, k, stream=s)))
+    torch.cuda.synchronize()
+    for k, out in got:
+        assert all(torch.equal(a, b) for a, b in zip(alone[k], out)), k
+    assert cuda_lib.get_device_error() == 0
+
+
+def test_states_beyond_32_bits_of_offset(cuda_lib):
+    """A pool of 2100 states of 128 heads: its last lie over 2^31 elements in (8.8 GB)."""
+    import torch
+    cfg = ref.config(nheads=128, ngroups=8)
+    g = on_gpu(ref.inputs(cfg, 2, 2, seed=6))
+    rows = [g[n] for n in ("q", "k", "v", "dt", "b")]
+    few = g["h0"].clone()
+    want = cuda_lib.delta_decode_step(cfg, *rows, g["A"], g["dt_bias"], few)
+    pool = torch.empty(2100, 128, 64, 128, device="cuda")
+    assert pool[:2099].numel() > 2 ** 31
+    slots = torch.tensor([2099, 2060], dtype=torch.int32, device="cuda")
+    pool[slots.long()] = g["h0"]
+    y = cuda_lib.delta_decode_step(cfg, *rows, g["A"], g["dt_bias"], pool, slots)
+    assert torch.equal(y, want) and torch.equal(pool[slots.long()], few)
+    cache, scales = cuda_lib.state_cache(2, (128, 64, 128))
+    ref_cache, ref_scales = cuda_lib.state_cache(2, (128, 64, 128))
+    cuda_lib.state_store(pool, cache, scales, state_slots=slots)
+    cuda_lib.state_store(few, ref_cache, ref_scales)
+    assert torch.equal(cache.view(torch.uint8), ref_cache.view(torch.uint8)) and torch.equal(scales, ref_scales)
+    cuda_lib.state_load(cache, scales, pool, state_slots=slots)
+    assert torch.equal(pool[2099], cuda_lib.state_load(cache, scales, few)[0])
+    assert cuda_lib.get_device_error() == 0
+
+
 @pytest.mark.parametrize("packed", [False, True])
 def test_no_tokens_need_only_the_states(cuda_lib, packed):
     """With no token at all, every pointer but the states' (and a packed call's workspace) may be null."""
@@ -311,8 +354,7 @@ def test_no_tokens_need_only_the_states(cuda_lib, packed):
 @pytest.mark.parametrize("kernel", [SIMT, TENSOR])
 def test_a_full_machine_gives_equal_bits(cuda_lib, kernel):
     """Many sequences at once, on every SM: the same bits whatever the workspace held and whatever the L2
-    cache holds.  On the tensor cores each sequence has the bits of its own call, too (in fp32 a small call
-    sums a row over eight lanes and a large one over four)."""
+    cache holds, and each sequence has the bits of its own call."""
     import torch
     cfg = ref.config(nheads=64, ngroups=8)
     r = np.random.default_rng(5)
@@ -328,7 +370,7 @@ def test_a_full_machine_gives_equal_bits(cuda_lib, kernel):
         got = run_packed(cuda_lib, cfg, g, cu, True, kernel, workspace=ws)
         first = first or got
         assert all(torch.equal(a, b) for a, b in zip(first, got)), i
-    for i in (0, 7, 23) if kernel == TENSOR else ():
+    for i in (0, 7, 23):
         part = {k: v[cu[i]:cu[i + 1]] if k in ("q", "k", "v", "dt", "b") else v for k, v in g.items()}
         part["h0"] = g["h0"][i:i + 1]
         y, h = run_packed(cuda_lib, cfg, part, [0, cu[i + 1] - cu[i]], True, kernel)
