@@ -392,9 +392,6 @@ __global__ void __launch_bounds__(WARPS * 32) delta_decode_kernel(const DeltaPla
   }
 }
 
-// 16 rows per CTA spread a small call over more SMs
-bool is_small(const DeltaPlan &p) { return (long long)p.B * p.H * p.P <= 64 * 2 * 148; }
-
 // The rows of a CTA: as few as leave one CTA per SM, since the rows of an SM share its shared-memory reads, and
 // as many as the registers allow once there are more.  Every choice gives the same bits.  256 tokens x H
 // heads of 64 rows, fp32, in us with CW = 2, 4, 8:  H = 8: 31, 38, 60;  32: 44, 40, 61;  64: 79, 75, 61;
@@ -410,9 +407,13 @@ cudaError_t launch_recurrent(const DeltaPlan &p, cudaStream_t s) {
   if (rows <= 8 * 148) return launch_rows<T, 2>(p, s);
   return rows <= 16 * 148 ? launch_rows<T, 4>(p, s) : launch_rows<T, 8>(p, s);
 }
+// Batches whose states stay in the L2 cache (64 MB of its 126) have eight lanes per row and 16 rows per CTA, which
+// spreads a small one over more SMs; larger ones four lanes, 64 rows, and stores past the cache.  In us, the
+// former and the latter: 1 row of 32 heads of 128 3.2 : 3.5, 5 rows 5.2 : 5.9, 20 rows (42 MB) 16.1 : 16.7; of 128
+// heads of 64 16 rows (67 MB) 24.3 : 24.5, 64 rows (268 MB) 99 : 90.
 template <typename T>
 cudaError_t launch_decode(const DeltaPlan &p, cudaStream_t s) {
-  if (is_small(p)) delta_decode_kernel<T, 8, 4><<<dim3(p.H * p.P / 16, p.B), 128, 0, s>>>(p);
+  if ((long long)p.B * p.H * p.P <= 131072) delta_decode_kernel<T, 8, 4><<<dim3(p.H * p.P / 16, p.B), 128, 0, s>>>(p);
   else delta_decode_kernel<T, 4, 8><<<dim3(p.H * p.P / 64, p.B), 256, 0, s>>>(p);
   return cudaGetLastError();
 }

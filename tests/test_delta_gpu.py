@@ -287,6 +287,28 @@ def test_first_calls_of_a_process_in_a_capture(cuda_lib):
     assert r.returncode == 0, r.stderr[-2000:]
 
 
+@pytest.mark.parametrize("headdim,dtype", [(64, "bf16"), (128, "f32")])
+def test_decode_of_a_large_batch(cuda_lib, headdim, dtype):
+    """More states than the L2 cache keeps (over 64 MB), in slots, some rows without one."""
+    import torch
+    cfg = ref.config(nheads=64, ngroups=8, headdim=headdim, dtype=dtype)
+    B = 131072 // (64 * headdim) + 3
+    d = ref.inputs(cfg, B, B, seed=21)
+    g = on_gpu(d)
+    slots = np.random.default_rng(3).permutation(B).astype(np.int32)
+    slots[4::9] = -1
+    state = g["h0"].clone()
+    y = cuda_lib.delta_decode_step(cfg, *(g[x] for x in ("q", "k", "v", "dt", "b")), g["A"], g["dt_bias"], state,
+                                   torch.from_numpy(slots).cuda())
+    S = d["h0"].astype(np.float64)
+    want = np.zeros((B, 64 * headdim))
+    for i, s in enumerate(slots):
+        if s >= 0:
+            want[i] = ref.rule(cfg, d, [i], S[s])[0]
+    ref.check_state(host(state), S, 1, "large")
+    ref.check_y(host(y), want, cfg, False, 1, "large")
+
+
 def test_two_calls_at_once(cuda_lib):
     """Chunked kernels and the recurrence on two streams at the same time: the bits of each alone."""
     import torch
