@@ -13,10 +13,14 @@ constexpr int kDeltaChunk = 64;
 //  tile    per (chunk, group): the fp16 operand image of 64 key and 64 query rows, 16 of each in turn, two
 //          halves of 64 columns, each 128 rows x 128 bytes with the 128-byte swizzle; then the row
 //          factors rho_k[64], rho_q[64] (fp32)
-//  record  per (chunk, head): the operand images of T~^T hi, T~^T lo and A T (64 rows x 128 bytes each,
-//          swizzled); then beta[64], 2^cs[64] and rho_k 2^{cs at the chunk's end - cs}[64] (fp32)
+//  record  per (chunk, head): the triangles of T~^T (its columns i >= its rows j) and A T (rows t >= columns j) as
+//          operand images in blocks of 16 rows x 16 columns, 512 bytes: [row / 8][column / 8][row % 8][column % 8]
+//          halves.  T~^T: for each 16 columns kb the row blocks 0 .. kb of hi, then of lo.  A T: for each 16
+//          columns kb the row blocks kb .. 3.  Then beta[64], 2^cs[64] and rho_k 2^{cs at the chunk's end - cs}[64]
+//          (fp32).
 constexpr long long kDeltaTileBytes = 32768 + 512;
-constexpr long long kDeltaRecordBytes = 3 * 8192 + 3 * 256;
+constexpr int kDeltaTBytes = 20 * 512, kDeltaATBytes = 10 * 512;
+constexpr long long kDeltaRecordBytes = kDeltaTBytes + kDeltaATBytes + 3 * 256;
 
 struct DeltaPlan {
   int B, L, H, P, G, hpg;  // L: the longest sequence of a packed batch

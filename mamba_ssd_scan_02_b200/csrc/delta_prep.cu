@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
       }
       const long long cs0 = sum - s[1] + s[0], cs1 = sum;
       const long long end = __shfl_sync(0xffffffffu, sum, 31);
-      float2 *o = reinterpret_cast<float2 *>(rec + 3 * 8192) + lane;
+      float2 *o = reinterpret_cast<float2 *>(rec + kDeltaTBytes + kDeltaATBytes) + lane;
       o[0] = make_float2(beta[0], beta[1]);
       o[32] = make_float2(exp2_fixed(cs0), exp2_fixed(cs1));
       o[64] = make_float2(rho.x * exp2_fixed(end - cs0), rho.y * exp2_fixed(end - cs1));
@@ -478,46 +478,34 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
       put_block<0, 4, 1>(w, d1, lane);
     }
     __syncwarp();
-    // T operands: 8 elements of a row per lane, of the blocks on and above the diagonal; hi also over the
-    // row in w, for A T
+    // T operands: 8 elements of a row per lane, of the blocks on and above the diagonal; hi also over the row in w,
+    // for A T.  A warp's 16 rows x 16 columns are one block of the image: 512 bytes in a row.
 #pragma unroll
     for (int half = 0; half < 2; ++half) {  // two blocks of 16 rows at a time: all reads first
-      constexpr uint4 zero = {0, 0, 0, 0};
-      float *row[7];
+      constexpr int kBlocks[2] = {4 + 3, 2 + 1};
+      const int j = lane & 15;
       float4 a[7], b[7];
 #pragma unroll
-      for (int k = 0; k < 7 - 4 * half; ++k) {
-        const int rb = 2 * half + (k >= 4 - 2 * half), units = 8 - 2 * rb, x = 32 * (k >= 4 - 2 * half ? k - 4 + 2 * half : k) + lane;
-        row[k] = w + row_start(16 * rb) + (x / units) * pitch(16 * rb) + 4 * (x % units);
-        // (the second four lanes of a row read their halves in the other order: else they meet the first's banks)
-        const float *src = row[k] + 4 * (x % units);
-        const int odd = (x % units) & 4;
-        const float4 f = *reinterpret_cast<const float4 *>(src + odd), g = *reinterpret_cast<const float4 *>(src + 4 - odd);
-        a[k] = odd ? g : f;
-        b[k] = odd ? f : g;
+      for (int k = 0; k < kBlocks[half]; ++k) {
+        const int rb = 2 * half + (k >= 4 - 2 * half), cb = k >= 4 - 2 * half ? k - 4 + 2 * half : k;  // columns 16 (rb + cb) ..
+        const float *src = w + row_start(16 * rb) + j * pitch(16 * rb) + 16 * cb + 8 * (lane >> 4);
+        a[k] = *reinterpret_cast<const float4 *>(src);
+        b[k] = *reinterpret_cast<const float4 *>(src + 4);
       }
       __syncwarp();
 #pragma unroll
-      for (int k = 0; k < 7 - 4 * half; ++k) {
-        const int rb = 2 * half + (k >= 4 - 2 * half), units = 8 - 2 * rb, x = 32 * (k >= 4 - 2 * half ? k - 4 + 2 * half : k) + lane;
-        const int j = 16 * rb + x / units, u = 2 * rb + x % units;
+      for (int k = 0; k < kBlocks[half]; ++k) {
+        const int rb = 2 * half + (k >= 4 - 2 * half), cb = k >= 4 - 2 * half ? k - 4 + 2 * half : k, kb = rb + cb;
         uint4 hv, lv;
         split2(make_float2(a[k].x, a[k].y), hv.x, lv.x);
         split2(make_float2(a[k].z, a[k].w), hv.y, lv.y);
         split2(make_float2(b[k].x, b[k].y), hv.z, lv.z);
         split2(make_float2(b[k].z, b[k].w), hv.w, lv.w);
-        *reinterpret_cast<uint4 *>(row[k]) = hv;
-        *reinterpret_cast<uint4 *>(rec + swz(j, u)) = hv;
-        *reinterpret_cast<uint4 *>(rec + 8192 + swz(j, u)) = lv;
+        *reinterpret_cast<uint4 *>(w + row_start(16 * rb) + j * pitch(16 * rb) + 8 * cb + 4 * (lane >> 4)) = hv;
+        unsigned char *dst = rec + 512 * (kb * (kb + 1) + rb) + (j >> 3) * 256 + (lane >> 4) * 128 + (j & 7) * 16;
+        *reinterpret_cast<uint4 *>(dst) = hv;
+        *reinterpret_cast<uint4 *>(dst + 512 * (kb + 1)) = lv;
       }
-#pragma unroll
-      for (int rb = 2 * half; rb < 2 * half + 2; ++rb)
-#pragma unroll
-        for (int x = lane; x < 32 * rb; x += 32) {
-          const int j = 16 * rb + (x & 15), u = x >> 4;
-          *reinterpret_cast<uint4 *>(rec + swz(j, u)) = zero;
-          *reinterpret_cast<uint4 *>(rec + 8192 + swz(j, u)) = zero;
-        }
     }
     __syncwarp();
     // A T: tiles on and below the diagonal.  Decays to a token of an earlier 16 in two factors, both at most
@@ -568,18 +556,16 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
           o[2 * k] = h2(__floats2half2_rn(c[0], c[1]));
           o[2 * k + 1] = h2(__floats2half2_rn(c[2], c[3]));
         }
-        stmatrix4(im + swz(16 * mt + (lane & 15), 2 * np + (lane >> 4)), o);
+        // block (np, mt) is the (4 np - np (np - 1) / 2 + mt - np)-th
+        stmatrix4(im + 512 * (3 * np - np * (np - 1) / 2 + mt) + (lane >> 3 & 1) * 256 + (lane >> 4) * 128 + (lane & 7) * 16, o);
       }
     }
     __syncwarp();
     // out by whole lines: written from the fragments, 16 bytes of 8 rows at a time, it would be four times the
     // requests
-#pragma unroll 4
-    for (int it = 0; it < 16; ++it) {
-      const int x = 32 * it + lane, t = x >> 3, u = (x ^ t) & 7;  // the unit that lies at x
-      const uint4 v = *reinterpret_cast<const uint4 *>(image + 16 * x);
-      reinterpret_cast<uint4 *>(rec + 2 * 8192)[x] = u >> 1 > t >> 4 ? make_uint4(0, 0, 0, 0) : v;
-    }
+#pragma unroll
+    for (int it = 0; it < 10; ++it)
+      *reinterpret_cast<uint4 *>(rec + kDeltaTBytes + 512 * it + 16 * lane) = *reinterpret_cast<const uint4 *>(image + 512 * it + 16 * lane);
     __syncwarp();
   }
 }

@@ -69,12 +69,14 @@ constexpr uint32_t OFF_RHOK = 2 * kHalf;          // the tile's row factors foll
 constexpr uint32_t OFF_RHOQ = OFF_RHOK + 256;
 constexpr uint32_t kTile = 33 * 1024;
 static_assert(OFF_RHOQ + 256 == kDeltaTileBytes && kDeltaTileBytes <= kTile, "as loaded");
-constexpr uint32_t kT = 16384, kAT = 8192;        // T~^T hi, lo; A T
+// T~^T: four times (16 columns) 64 rows of hi, 64 of lo, 32 bytes each; A T: four times (16 columns) 128 rows,
+// 16 of each of two chunks in turn.  In 8 x 8 core matrices; what the triangles leave out stays zero.
+constexpr uint32_t kT = 16384, kAT = 8192;
 constexpr uint32_t OFF_BETA = 8192;               // after V (64 rows of 128 bytes, swizzled): three arrays of 64 floats
 constexpr uint32_t OFF_GAMMA = OFF_BETA + 256;
 constexpr uint32_t OFF_END = OFF_GAMMA + 256;
 constexpr uint32_t kVG = 9 * 1024;
-static_assert(kT + kAT + 3 * 256 == kDeltaRecordBytes && OFF_END + 256 <= kVG, "as loaded");
+static_assert(OFF_END + 256 <= kVG, "as loaded");
 // CTA
 constexpr uint32_t OFF_T = kDeep * kTile;
 constexpr uint32_t OFF_AT = OFF_T + 2 * kT;
@@ -174,6 +176,7 @@ struct Ring {
 // below 256 KB); the other word holds the strides, the version bits and the 128-byte swizzle.
 __device__ __forceinline__ uint32_t op_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | (lbo >> 4) << 16; }
 constexpr uint32_t kOpHi = 1024 >> 4 | 1u << 14 | 2u << 29;
+constexpr uint32_t kCoreHi = 256 >> 4 | 1u << 14;  // the same for rows of 8 x 8 core matrices, two of them 16 columns
 __device__ __forceinline__ constexpr uint32_t kstep(int j) { return ((j >> 2) * kHalf + (j & 3) * 32) >> 4; }
 __device__ __forceinline__ constexpr uint32_t tstep(int j) { return 16 * j; }
 
@@ -181,16 +184,16 @@ __device__ __forceinline__ constexpr uint32_t tstep(int j) { return 16 * j; }
 // broadcast with shuffles: the compiler then knows it to be uniform and keeps the descriptors in uniform
 // registers.  Moved there from a divergent branch for every MMA, they cost 50 to 80 clocks each, more
 // than the MMA (SS N = 64: 49 clocks, its operands' shared-memory reads; TS N = 64: 32, N = 32: 16).
-template <uint32_t kIdesc>
+template <uint32_t kIdesc, uint32_t kAHi = kOpHi, uint32_t kBHi = kOpHi>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, bool acc) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
       "mov.b64 x, {%1, %5};\n\t"
-      "mov.b64 y, {%2, %5};\n\t"
+      "mov.b64 y, {%2, %6};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "n"(kIdesc), "r"((uint32_t)acc), "n"(kOpHi)
+      "r"(a), "r"(b), "n"(kIdesc), "r"((uint32_t)acc), "n"(kAHi), "n"(kBHi)
       : "memory");
 }
 template <uint32_t kIdesc>
@@ -219,9 +222,9 @@ __device__ __forceinline__ void issue_D1(uint32_t kq, uint32_t sbuf, uint32_t d)
   for (int j = 0; j < 8; ++j) mma_ss<IDESC_D1>(d, a + kstep(j), b + j * 128, j > 0);
 }
 __device__ __forceinline__ void issue_M(uint32_t kq, uint32_t t, uint32_t d) {
-  const uint32_t a = op_lo(kq, kHalf), b = op_lo(t, 16);
+  const uint32_t a = op_lo(kq, kHalf), b = op_lo(t, 128);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) mma_ss<IDESC_M>(d, a + j * 256, b + j * 2, j > 0);  // 16 K rows of every 32
+  for (int j = 0; j < 4; ++j) mma_ss<IDESC_M, kOpHi, kCoreHi>(d, a + j * 256, b + j * 256, j > 0);  // 16 K rows of every 32
 }
 // d = M_lo R_hi + M_hi R_lo + M_hi R_hi  (64 tokens; the small ones first).  The half's columns of R begin
 // 64 half bytes into its rows.
@@ -236,11 +239,11 @@ __device__ __forceinline__ void issue_S(uint32_t m, uint32_t r, int half, uint32
   for (int j = 0; j < 4; ++j) mma_ts<IDESC_S>(d, m + tstep(j), hi + 128 * j, true);
 }
 // A T . R_hi.  The rows of A T are the second 16 of every 32 rows of the A operand; the first 16 are the other
-// chunk's (or, before the first place, the end of T), and their results are not used.
+// chunk's (or what lies before the first place), and their results are not used.
 __device__ __forceinline__ void issue_O(uint32_t at, uint32_t r, uint32_t d) {
-  const uint32_t a = op_lo(at - 2048, 16), b = op_lo(r, 8192);
+  const uint32_t a = op_lo(at - 512, 128), b = op_lo(r, 8192);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) mma_ss<IDESC_O>(d, a + 2 * j, b + 128 * j, j > 0);
+  for (int j = 0; j < 4; ++j) mma_ss<IDESC_O, kCoreHi, kOpHi>(d, a + 256 * j, b + 128 * j, j > 0);
 }
 
 // 16 TMEM lanes (from taddr's on) x 32 columns: thread l has of rows l / 4 and l / 4 + 8 the columns 8 b + 2 (l % 4) and
@@ -299,6 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     misc[1] = misc[2] = 0;
     fence_mbar_init();
   }
+  for (uint32_t i = tid * 16; i < 2 * kT + 2 * kAT; i += kThreads * 16)  // T and A T: what is never loaded
+    *reinterpret_cast<uint4 *>(smem + OFF_T + i) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
   if (warp == 13) {
     tmem_alloc(sb + OFF_MISC, TM_COLS);
     tmem_relinquish();
@@ -623,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait2(BAR_AT, k) && ok;
         ok = wait(BAR_QREAD, k & 1) && ok;
         tc_fence_after();
-        issue_O(sb + OFF_AT + (k & 1) * 2048, sb + OFF_R, tmem + TM_O);
+        issue_O(sb + OFF_AT + (k & 1) * 512, sb + OFF_R, tmem + TM_O);
         commit(BAR(BAR_O));
         commit(BAR(BAR_EMPTY + r.at));
         ok = __all_sync(0xffffffffu, ok);
@@ -663,10 +669,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const unsigned char *before = nullptr;  // A T of the chunk before
       const auto load_at = [&](const unsigned char *src) {
         const uint32_t at = BAR(BAR_AT + (n_at & 1));
-        mbar_arrive_expect_tx(at, kAT);
+        mbar_arrive_expect_tx(at, kDeltaATBytes);
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j)  // the two places alternate by 16 rows
-          bulk_load(sb + OFF_AT + (n_at & 1) * 2048 + j * 4096, src + j * 2048, 2048, at);
+        for (int kb = 0; kb < 4; ++kb)
+#pragma unroll 1
+          for (int g = kb; g < 4; ++g, src += 512)  // the two places alternate by 16 rows
+            bulk_load(sb + OFF_AT + kb * 4096 + g * 1024 + (n_at & 1) * 512, src, 512, at);
         ++n_at;
       };
       // Chunk k's turn: its tile, V and gates, into the place of chunk k - 3; A T of chunk k - 1 (and in turn 0 of
@@ -677,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int seq = seq_at(rank), h = hp >> (p.P > 64), nck = (seq_len(p.cu, seq, p.L) + C - 1) / C;
         const long long base = seq_base(p.cu, seq, p.L);
         const long long ck0 = p.chunk0 ? p.chunk0[seq] : (long long)seq * nck;
-        const unsigned char *rec = p.records + (ck0 * p.H + h) * kDeltaRecordBytes + kT;
+        const unsigned char *rec = p.records + (ck0 * p.H + h) * kDeltaRecordBytes + kDeltaTBytes;
         const unsigned char *tile = p.tiles + (ck0 * p.G + h / p.hpg) * kDeltaTileBytes;
         for (int c = 0; c < nck; ++c, rec += rec_step, tile += tile_step) {
           if (n >= kDeep) {
@@ -694,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
           mbar_arrive_expect_tx(tb, (uint32_t)kDeltaTileBytes);
           bulk_load(sb + r.at * kTile, tile, (uint32_t)kDeltaTileBytes, tb);
-          bulk_load(dst + OFF_BETA, rec + kAT, 768, vg);
+          bulk_load(dst + OFF_BETA, rec + kDeltaATBytes, 768, vg);
           r.next();
           if (n != 1) load_at(n == 0 ? rec : before);
           before = rec;
@@ -761,8 +769,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k == -2 && lead) asm volatile("griddepcontrol.wait;" ::: "memory");
         if (lead) {
           const uint32_t t = BAR(BAR_T + (k & 1));
-          mbar_arrive_expect_tx(t, kT);
-          bulk_load(sb + OFF_T + (k & 1) * kT, rec, kT, t);
+          mbar_arrive_expect_tx(t, kDeltaTBytes);
+          const unsigned char *src = rec;
+          uint32_t dst = sb + OFF_T + (k & 1) * kT, bytes = 512;
+#pragma unroll 1
+          for (int kb = 0; kb < 4; ++kb, dst += 4096, bytes += 512) {
+            bulk_load(dst, src, bytes, t);
+            bulk_load(dst + 2048, src + bytes, bytes, t);
+            src += 2 * bytes;
+          }
         }
         rows_next = min(C, len - c * C);
         rec += p.H * kDeltaRecordBytes;
