@@ -10,17 +10,17 @@
 //   T~     = (I + L~)^-1, L~_ij = beta_i rho_i^2 K_i.K_j (j < i), in fp32: 16 x 16 diagonal blocks by
 //          substitution, joined by block products with tf32 in two parts (22 bits)
 //   A T    2^{cs_t - cs_j} rho_j (A~ T~)_tj, rounded once to fp16
-// and leaves T~ in two fp16 parts and A T as the swizzled operand images that the chunk kernel loads.
+// and leaves the triangles of T~ in two fp16 parts and of A T as the operand images that the chunk kernel loads.
 //
 // Why apart from the chunk kernel: inside it this part ran in the same SM as the tcgen05 products, which
 // slow mma.sync down threefold and shared-memory loads twofold, and its latency (about 5 us a chunk)
-// bounded every CTA: 650 us for 8192 tokens x 128 heads, where the two kernels now take 130 and 217.  Here it
+// bounded every CTA: 650 us for 8192 tokens x 128 heads, where the two kernels now take 121 and 220.  Here it
 // is spread over all chunks, twelve independent warps per SM (three CTAs; two of them with rows of one
-// pitch: 154 us).  The price is 25 KB of workspace per chunk and head, written once and read once.
+// pitch: 154 us).  The price is 16 KB of workspace per chunk and head, written once and read once.
 //
-// What bounds it (8192 tokens x 128 heads, 16384 heads' chunks: 130 us): the shared-memory and store pipe, two
-// thirds busy; 43 % of the issue slots are used, 40 % of the DRAM rate.  Its 404 MB of records alone would
-// take 62 us.  As many heads per CTA as share K K^T (16; 8: 166 us where 16 took 154): the K and Q part costs
+// What bounds it (8192 tokens x 128 heads, 16384 heads' chunks: 121 us): the shared-memory and store pipe, two
+// thirds busy; 40 % of the issue slots are used, 31 % of the DRAM rate.  Its 264 MB of records alone would
+// take 40 us.  As many heads per CTA as share K K^T (16; 8: 166 us where 16 took 154): the K and Q part costs
 // as much as one head.
 #include "common.cuh"
 #include "delta_mma.cuh"

@@ -35,10 +35,10 @@
 // of each chunk.  Hand-overs are mbarriers; every wait is bounded: a timeout makes every role leave and
 // latches SSD_ERR_TIMEOUT.
 //
-// What bounds it: the chain.  A chunk takes 1.7 us (8192 tokens x 128 heads: 217 us on 128 SMs; 245 at the clocks
+// What bounds it: the chain.  A chunk takes 1.7 us (8192 tokens x 128 heads: 220 us on 128 SMs; 245 at the clocks
 // that a second of such calls leaves): S into fp16 0.25 (the halves one after the other 0.5), K S^T 0.4, R 0.25,
-// M R 0.35 (the next rows load meanwhile), the new S 0.2; the tensor pipe is 53 % busy, the issue slots 56 %, DRAM
-// 36 %.  Measured against it, at the stage each was tried: y by the chain's warps 246 us where this took 226;
+// M R 0.35 (the next rows load meanwhile), the new S 0.2; the tensor pipe is 53 % busy, the issue slots 59 %, DRAM
+// 27 %.  Measured against it, at the stage each was tried: y by the chain's warps 246 us where this took 226;
 // M R waiting for the readers of Q S^T 226 : 213; one M R for both halves 246 : 226; a product per half for
 // K S^T (the halves half a chunk apart, one issuer each or one for both) 255 to 260 : 232, since the K and Q
 // operand is then read twice.  The code is kept small (loops rolled, one place per inlined part): sixteen
