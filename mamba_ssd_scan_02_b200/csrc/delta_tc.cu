@@ -329,9 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *max_s = reinterpret_cast<uint32_t *>(smem + OFF_MAXS) + 12 * hf;
     const uint32_t t_d1 = tmem + TM_D1 + 64 * hf, t_s = tmem + TM_S + 32 * hf;
     float2 S[16];  // the state, times sc.x
-    int len = 0;             // of the item: tokens, the first of them's row, and h P + the first state row
-    long long base = 0;
-    int hp = 0;
+    int len = 0;   // the item's tokens
     const auto publish_max = [&](int buf) {
       float top = 0.f;
 #pragma unroll
@@ -374,8 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k = 0, fulls = 0;  // chunks; items with chunks
     int seq = 0, hp_next = 0;  // of the next item
     for (uint32_t i = blockIdx.x; i < n_items + step && ok; i += step) {
-      const int seq_now = seq;
-      hp = hp_next;
+      const int seq_now = seq, hp = hp_next;
       if (i < n_items) {  // on its way while the item before runs
         const uint32_t rank = i / per_seq;
         seq = seq_at(rank);
@@ -383,7 +380,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (i < step) continue;
       len = seq_len(p.cu, seq_now, p.L);
-      base = seq_base(p.cu, seq_now, p.L);
       const int nck = (len + C - 1) / C;
       const long long soff = ((long long)seq_now * p.H * p.P + hp + 32 * hf) * kDState + n;
 #pragma unroll
