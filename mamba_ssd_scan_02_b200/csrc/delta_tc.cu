@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return ok;
     };
     bool ok = true;
-    int k = 0, fulls = 0;  // chunks; items with chunks
+    int k = 0, fulls = 0;  // chunks; items with chunks and an initial state
     int seq = 0, hp_next = 0;  // of the next item
     for (uint32_t i = blockIdx.x; i < n_items + step && ok; i += step) {
       const int seq_now = seq, hp = hp_next;
@@ -389,8 +389,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 16; ++j) S[j] = make_float2(src[(2 * j) * kDState], src[(2 * j + 1) * kDState]);
       }
+      if (nck == 0) {  // no tokens: the state goes on as it came, of any size
+        if (p.h_final && in_bounds(soff + 31 * kDState, p.state_extent, p.err))
+#pragma unroll
+          for (int j = 0; j < 32; ++j) p.h_final[soff + j * kDState] = j & 1 ? S[j / 2].y : S[j / 2].x;
+        continue;
+      }
       m = 0.f;
-      if (p.h0 && nck > 0) {
+      if (p.h0) {
         publish_max(2);
         if (lead) mbar_arrive(BAR(BAR_MAX + hf));
         ok = wait(BAR_MAX + hf, fulls++ & 1);
@@ -400,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sc = state_scale(m);
 #pragma unroll
       for (int j = 0; j < 16; ++j) S[j] = __fmul2_rn(S[j], make_float2(sc.x, sc.x));
-      if (nck > 0) ok = load_rows(0) && ok;
+      ok = load_rows(0) && ok;
       for (int c = 0;; ++c, ++k) {
         if (c < nck) {
           // S into its operand
