@@ -469,7 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        m = fmaf(decay, read_max(k & 1), bound);
+        // (not so far below the scale of R that the factor between the two overflows: a decay of the state to
+        // zero in a chunk without values)
+        m = max_bound(fmaf(decay, read_max(k & 1), bound), 0x1p-90f * 64.f * rsc.y);
         sc = state_scale(m);
         const float ge = decay * sc.x, yn = rsc.y * sc.x;
         const float2 ge2 = make_float2(ge, ge), y2 = make_float2(yn, yn);
