@@ -294,9 +294,12 @@ typedef struct {
 size_t ssd_delta_workspace_size(const ssd_delta_config_t *cfg);
 
 /* y and the final state of seqlen tokens per batch row.  Consecutive calls, each fed the previous
- * call's h_final, give the result of one call (up to rounding).  Accuracy: the state within about
- * 1e-6 of its size of the fp32 recurrence's, on both paths; y rounded once into io_dtype, from
- * products that keep 11 bits within a chunk on the chunked path. */
+ * call's h_final, give the result of one call (up to rounding).  Accuracy, head by head: the state within
+ * about 1e-6 (root mean square) of the largest thing it was made of - the state that came in, each token's
+ * beta |k^| |v|, each state on the way - as decayed since, on both paths (a few 1e-6 where keys of very different
+ * sizes or decays of e^-10 and less a token meet); on the chunked one a decay below 2^-126 within 64 tokens is
+ * zero.  y rounded once into io_dtype; on the chunked path what a token adds to the y of its own
+ * chunk of 64 keeps 11 bits, or an error of 2^-24 of the largest such term of its chunk and head. */
 ssd_status_t ssd_delta_prefill(const ssd_delta_config_t *cfg, const ssd_delta_args_t *args, void *stream);
 
 /* Packed sequences, as in ssd_prefill_varlen: cu_seqlens is a HOST array of nseq + 1 offsets (read

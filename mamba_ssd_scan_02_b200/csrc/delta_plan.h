@@ -16,8 +16,8 @@ constexpr int kDeltaChunk = 64;
 //  record  per (chunk, head): the triangles of T~^T (its columns i >= its rows j) and A T (rows t >= columns j) as
 //          operand images in blocks of 16 rows x 16 columns, 512 bytes: [row / 8][column / 8][row % 8][column % 8]
 //          halves.  T~^T: for each 16 columns kb the row blocks 0 .. kb of hi, then of lo.  A T: for each 16
-//          columns kb the row blocks kb .. 3.  Then beta[64], 2^cs[64] and rho_k 2^{cs at the chunk's end - cs}[64]
-//          (fp32).
+//          columns kb the row blocks kb .. 3.  Then u = beta rho_k [64], 2^cs [64] and w = u 2^{cs at the chunk's
+//          end - cs} [64] (fp32).
 constexpr long long kDeltaTileBytes = 32768 + 512;
 constexpr int kDeltaTBytes = 20 * 512, kDeltaATBytes = 10 * 512;
 constexpr long long kDeltaRecordBytes = kDeltaTBytes + kDeltaATBytes + 3 * 256;

@@ -9,7 +9,7 @@
 //          exact however large the sums
 //   T~     = (I + L~)^-1, L~_ij = beta_i rho_i^2 K_i.K_j (j < i), in fp32: 16 x 16 diagonal blocks by
 //          substitution, joined by block products with tf32 in two parts (22 bits)
-//   A T    2^{cs_t - cs_j} rho_j (A~ T~)_tj, rounded once to fp16
+//   A T    2^{cs_t - cs_j} (A~ T~)_tj, at most 529 in size, rounded once to fp16
 // and leaves the triangles of T~ in two fp16 parts and of A T as the operand images that the chunk kernel loads.
 //
 // Why apart from the chunk kernel: inside it this part ran in the same SM as the tcgen05 products, which
@@ -432,18 +432,19 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
       const long long cs0 = sum - s[1] + s[0], cs1 = sum;
       const long long end = __shfl_sync(0xffffffffu, sum, 31);
       float2 *o = reinterpret_cast<float2 *>(rec + kDeltaTBytes + kDeltaATBytes) + lane;
-      o[0] = make_float2(beta[0], beta[1]);
+      const float2 u = make_float2(beta[0] * rho.x, beta[1] * rho.y);
+      o[0] = u;
       o[32] = make_float2(exp2_fixed(cs0), exp2_fixed(cs1));
-      o[64] = make_float2(rho.x * exp2_fixed(end - cs0), rho.y * exp2_fixed(end - cs1));
+      o[64] = make_float2(u.x * exp2_fixed(end - cs0), u.y * exp2_fixed(end - cs1));
       *reinterpret_cast<float2 *>(s_f + 2 * lane) = make_float2(-beta[0] * rho.x * rho.x, -beta[1] * rho.y * rho.y);
-      // for A T: cs relative to the first token of its 16; rho 2^(that - cs) for the tokens before
+      // for A T: cs relative to the first token of its 16; 2^(that - cs) for the tokens before
       long long ref[4];
 #pragma unroll
       for (int tb = 1; tb < 4; ++tb) {
         ref[tb] = __shfl_sync(0xffffffffu, cs0, 8 * tb);
         if (lane < 8 * tb)
           *reinterpret_cast<float2 *>(s_col + 8 * tb * (tb - 1) + 2 * lane) =
-              make_float2(rho.x * exp2_fixed(ref[tb] - cs0), rho.y * exp2_fixed(ref[tb] - cs1));
+              make_float2(exp2_fixed(ref[tb] - cs0), exp2_fixed(ref[tb] - cs1));
       }
       ref[0] = __shfl_sync(0xffffffffu, cs0, 0);
       const long long mine = lane < 16 ? (lane < 8 ? ref[0] : ref[1]) : (lane < 24 ? ref[2] : ref[3]);
@@ -546,12 +547,12 @@ __global__ void __launch_bounds__(kThreads, 3) ssd_delta_front_kernel(const Delt
             c[2] *= rt1 * f.x;
             c[3] *= rt1 * f.y;
           } else {
-            const float2 d = *reinterpret_cast<const float2 *>(s_rel + j), r = *reinterpret_cast<const float2 *>(s_rho + j);
+            const float2 d = *reinterpret_cast<const float2 *>(s_rel + j);
             // (above the diagonal the products are zero, and the decays could overflow)
-            c[0] *= r.x * ex2(j <= t ? d0 - d.x : 0.f);
-            c[1] *= r.y * ex2(j + 1 <= t ? d0 - d.y : 0.f);
-            c[2] *= r.x * ex2(j <= t + 8 ? d1 - d.x : 0.f);
-            c[3] *= r.y * ex2(j + 1 <= t + 8 ? d1 - d.y : 0.f);
+            c[0] *= ex2(j <= t ? d0 - d.x : 0.f);
+            c[1] *= ex2(j + 1 <= t ? d0 - d.y : 0.f);
+            c[2] *= ex2(j <= t + 8 ? d1 - d.x : 0.f);
+            c[3] *= ex2(j + 1 <= t + 8 ? d1 - d.y : 0.f);
           }
           o[2 * k] = h2(__floats2half2_rn(c[0], c[1]));
           o[2 * k + 1] = h2(__floats2half2_rn(c[2], c[3]));

@@ -8,24 +8,29 @@
 // K_i exact in fp16.  The decays and the rho are a similarity of L: with
 //   L~_ij = beta_i rho_i^2 K_i.K_j  (j < i),   T~ = (I + L~)^-1,
 // (I + L)^-1_ij = T~_ij 2^{cs_i - cs_j} rho_j / rho_i, so that
-//   S' = 2^{cs_C} S + sum_j R_j (rho_j 2^{cs_C - cs_j} M_j)^T,          M = K^T T~          (N x 64)
-//   y_t = 2^{cs_t} S q_t + sum_j 2^{cs_t - cs_j} rho_j (A~ T~)_tj R_j,   A~_ti = q_t.K_i     (i <= t)
+//   X_j = v_j - 2^{cs_j} S k_j,   u_j = beta_j rho_j,   w_j = 2^{cs_C - cs_j} u_j,
+//   S' = 2^{cs_C} S + sum_j (w_j X_j) M_j^T,                         M = K^T T~            (N x 64)
+//   y_t = 2^{cs_t} S q_t + sum_j 2^{cs_t - cs_j} (A~ T~)_tj (u_j X_j),   A~_ti = q_t.K_i     (i <= t)
 // The inverse, M and A~ T~ know no decay, and nothing of them depends on the state: the chain from chunk
-// to chunk is two dependent products, K S^T (which gives R) and M R.  A CTA carries 64 state rows of one head
+// to chunk is two dependent products, K S^T (which gives R = w X) and M R.  A CTA carries 64 state rows of one head
 // through a sequence (the rows are independent given K, so a head of 128 rows is two such items), then the next
 // item's: the grid is one CTA per SM, and an item's first loads and M run while the one before ends (64
 // sequences of up to 700 tokens x 128 heads: 715 us with a CTA per item, 610 so).
 //
-// The front end (delta_prep.cu) computes T~ and A T = 2^{cs_t - cs_j} rho_j (A~ T~)_tj.
+// The front end (delta_prep.cu) computes T~, A T = 2^{cs_t - cs_j} (A~ T~)_tj, u and w.
 //
 // Precision.  The state is fp32, in registers.  Its products run on fp16 operands in two parts,
 // hi = fp16(x), lo = fp16(x - hi), which keep 22 bits; the products hi.hi + hi.lo + lo.hi leave an error
 // of about 2^-22, so the state stays as near to the fp64 rule as an fp32 recurrence does.  K and Q need
 // one part: a row of bf16 numbers times a power of two is exact in fp16, and the power and the norm's
-// factor come back in the fp32 factors rho.  |T~| and |M| are bounded (beta |k|^2 <= 2 and
-// 1 <= |K_i| < 23); S and R are scaled by powers of two from running bounds of |S| and |V|
-// (state_scale), so that fp16's range holds any size of input.  Only what goes into y alone (A~, A T, the R
-// beside it) is rounded to 11 bits: y is then rounded to bf16's 8.
+// factor come back in the fp32 factors rho.  What differs in size between tokens and heads - beta, the decays, the
+// rho - stands in R, in fp32 before it is split: |T~|, |M| and |A T| are bounded without it (beta |k|^2 <= 2, 1 <=
+// |K_i| < 23, alpha <= 1), and R and the next S have one scale, the power of two of a bound of the next S that
+// counts each token's value as what is left of it at the chunk's end (state_scale).  So a term loses bits only
+// beside larger terms of the same state.  (With the factors in M, which had no scale, and R's scale from |S| and |V|
+// alone, a chunk that ended in tokens of small beta or without values lost up to all of the state's bits.)  Only
+// what goes into y alone (A~, A T, the R beside it: u X, scaled by the largest |S| and |u V|) is rounded to 11 bits,
+// each product below 2^-24 of the chunk's largest to fewer: y is then rounded to bf16's 8.
 //
 // Roles (16 warps, so that a thread may have 128 registers).  Warps 0-7, the chain: S into its operand, R
 // from K S^T, the new S.  Their two halves, 32 state rows each, share the product with K, whose operand is
@@ -72,39 +77,41 @@ static_assert(OFF_RHOQ + 256 == kDeltaTileBytes && kDeltaTileBytes <= kTile, "as
 // T~^T: four times (16 columns) 64 rows of hi, 64 of lo, 32 bytes each; A T: four times (16 columns) 128 rows,
 // 16 of each of two chunks in turn.  In 8 x 8 core matrices; what the triangles leave out stays zero.
 constexpr uint32_t kT = 16384, kAT = 8192;
-constexpr uint32_t OFF_BETA = 8192;               // after V (64 rows of 128 bytes, swizzled): three arrays of 64 floats
-constexpr uint32_t OFF_GAMMA = OFF_BETA + 256;
-constexpr uint32_t OFF_END = OFF_GAMMA + 256;
+constexpr uint32_t OFF_U = 8192;                  // after V (64 rows of 128 bytes, swizzled): three arrays of 64 floats
+constexpr uint32_t OFF_GAMMA = OFF_U + 256;
+constexpr uint32_t OFF_W = OFF_GAMMA + 256;
 constexpr uint32_t kVG = 9 * 1024;
-static_assert(OFF_END + 256 <= kVG, "as loaded");
+static_assert(OFF_W + 256 <= kVG, "as loaded");
 // CTA
 constexpr uint32_t OFF_T = kDeep * kTile;
 constexpr uint32_t OFF_AT = OFF_T + 2 * kT;
 constexpr uint32_t OFF_VG = OFF_AT + 2 * kAT;
-constexpr uint32_t OFF_SB = OFF_VG + kDeep * kVG;  // S operands of the halves: [n][32 p hi, 32 p lo], 128 rows each
-constexpr uint32_t OFF_R = OFF_SB + 2 * kHalf;    // R operands: [token][32 p of each half], 64 rows of hi, 64 of lo
-constexpr uint32_t OFF_MAXS = OFF_R + 2 * 8192;      // largest |S| per chain warp: two chunks, an item's first
-constexpr uint32_t OFF_SCALE = OFF_MAXS + 128;    // per half and chunk parity: the scales of S and R, backwards
-constexpr uint32_t OFF_MAXV = OFF_SCALE + 32;     // bound of what the chunk adds, per place in the ring
-constexpr uint32_t OFF_BAR = OFF_MAXV + 64;
+// Per half, S operand: [n][32 p hi, 32 p lo], 128 rows.  Once K S^T is done, R operand: [token][32 p hi, 32 p lo],
+// 64 rows.
+constexpr uint32_t OFF_SB = OFF_VG + kDeep * kVG;
+constexpr uint32_t OFF_R = OFF_SB + 2 * kHalf;    // R operand of y: [token][32 p of each half], 64 rows
+constexpr uint32_t OFF_MAXS = OFF_R + 8192;       // largest |S| per chain warp: two chunks, an item's first
+constexpr uint32_t OFF_SCALE = OFF_MAXS + 128;    // per half and chunk parity: the scales of S and of y's R, backwards
+constexpr uint32_t OFF_BOUND = OFF_SCALE + 32;    // per place in the ring: 4 max |w V|, max |u V|, the first 2^cs, the last
+constexpr uint32_t OFF_BAR = OFF_BOUND + 64;
 // A barrier that can complete again before every waiter has seen the phase before has one copy per
 // buffer, so that a parity test never sees two phases at once.
 enum {
   BAR_TILE,                        // [3] tile loaded
   BAR_VG = BAR_TILE + kDeep,       // [3] V and gates loaded
-  BAR_READY = BAR_VG + kDeep,      // [3] both, and the bound of what the chunk adds known
+  BAR_READY = BAR_VG + kDeep,      // [3] both, and the bounds of what the chunk adds known
   BAR_EMPTY = BAR_READY + kDeep,   // [3] the chunk's last product (and every read before it) is done
   BAR_T = BAR_EMPTY + kDeep,       // [2] T loaded
   BAR_AT = BAR_T + 2,              // [2] A T loaded
   BAR_M = BAR_AT + 2,              // [2] M done
   BAR_MREADY = BAR_M + 2,          // [2] M operand in tensor memory (4 warps)
   BAR_SREADY = BAR_MREADY + 2,     // S operand written (8 warps)
-  BAR_RREADY = BAR_SREADY + 1,     // [2 halves] R operand written, K S^T read (4 warps)
+  BAR_RREADY = BAR_SREADY + 1,     // [2 halves] R operands written, K S^T read (4 warps)
   BAR_D1 = BAR_RREADY + 2,         // K S^T, Q S^T done
   BAR_S = BAR_D1 + 1,              // [2 halves] M R done
   BAR_O = BAR_S + 2,               // A T R done
   BAR_DONE = BAR_O + 1,            // [2] nothing of an issuer's left in flight
-  BAR_MAX = BAR_DONE + 2,          // [2 halves] the bounds of an item's first state written (4 warps)
+  BAR_MAX = BAR_DONE + 2,          // [2 halves] the largest |S| of each warp written (4 warps)
   BAR_QREAD = BAR_MAX + 2,         // Q S^T read, and the y before it done (4 warps)
   kNumBars = BAR_QREAD + 1
 };
@@ -125,7 +132,7 @@ constexpr uint32_t TM_M = 0, TM_D1 = 256, TM_S = 384, TM_O = 448, TM_COLS = 512;
 constexpr uint32_t IDESC_D1 = idesc_f16(128, 128, false, true, kFmtF16);  // [K; Q] . S of both halves
 constexpr uint32_t IDESC_M = idesc_f16(128, 128, true, false, kFmtF16);   // K^T . [T_hi, T_lo]
 constexpr uint32_t IDESC_S = idesc_f16(128, 32, false, true, kFmtF16);    // M (TMEM) . R of a half
-constexpr uint32_t IDESC_O = idesc_f16(128, 64, false, true, kFmtF16);    // A T . R_hi of both halves
+constexpr uint32_t IDESC_O = idesc_f16(128, 64, false, true, kFmtF16);    // A T . R of both halves
 
 // A bounded wait.  A try suspends the warp for up to 7800 clocks (4 us); after every 256 the abort flag is
 // looked at, and after 2^11 times that (two seconds) the flag is set to 2.  In one piece of
@@ -226,10 +233,10 @@ __device__ __forceinline__ void issue_M(uint32_t kq, uint32_t t, uint32_t d) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) mma_ss<IDESC_M, kOpHi, kCoreHi>(d, a + j * 256, b + j * 256, j > 0);  // 16 K rows of every 32
 }
-// d = M_lo R_hi + M_hi R_lo + M_hi R_hi  (64 tokens; the small ones first).  The half's columns of R begin
-// 64 half bytes into its rows.
-__device__ __forceinline__ void issue_S(uint32_t m, uint32_t r, int half, uint32_t d) {
-  const uint32_t hi = op_lo(r, 8192) + 4 * half, lo = op_lo(r + 8192, 8192) + 4 * half;
+// d = M_lo R_hi + M_hi R_lo + M_hi R_hi  (64 tokens; the small ones first).  The lo columns of R begin 64 bytes into
+// its rows.
+__device__ __forceinline__ void issue_S(uint32_t m, uint32_t r, uint32_t d) {
+  const uint32_t hi = op_lo(r, 8192), lo = hi + 4;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     mma_ts<IDESC_S>(d, m + tstep(j) + 8, hi + 128 * j, j > 0);
@@ -238,7 +245,7 @@ __device__ __forceinline__ void issue_S(uint32_t m, uint32_t r, int half, uint32
 #pragma unroll
   for (int j = 0; j < 4; ++j) mma_ts<IDESC_S>(d, m + tstep(j), hi + 128 * j, true);
 }
-// A T . R_hi.  The rows of A T are the second 16 of every 32 rows of the A operand; the first 16 are the other
+// A T . R.  The rows of A T are the second 16 of every 32 rows of the A operand; the first 16 are the other
 // chunk's (or what lies before the first place), and their results are not used.
 __device__ __forceinline__ void issue_O(uint32_t at, uint32_t r, uint32_t d) {
   const uint32_t a = op_lo(at - 512, 128), b = op_lo(r, 8192);
@@ -263,8 +270,10 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float (&v)[16]) {
 
 // Powers of two that bring a quantity bounded by m to [64, 128) and back.  Headroom: with alpha <= 1
 // and beta |k|^2 <= 2 the transition does not expand a state row s, so over a chunk
-// |s'| <= gamma |s| + 64 * 2 max|V|, and |R| <= 2 (max|V| + |s|).  With m = gamma max|S_old| + max|V| that
-// is |S| <= (sqrt(128) + 128) m < 140 m and |R| < 282 max(m, max|V|): both below 65504 / 128 = 511.
+// |s'| <= gamma |s| + 64 max |w V| max |K|, with |K| < 23 and, of 128 elements, |s| <= 12 max |S|; and
+// |w X| <= max |w V| + 2 gamma |s|, since w_j 2^{cs_j} rho_j |K_j| = gamma beta_j |k_j|^2 / |K_j| <= 2 gamma.  With
+// m = gamma max |S| + 4 max |w V| the next state and R are below 380 m.  The R of y is below 25 times the larger of
+// max |u V| and 2^{cs_0} max |S|, what the first token leaves of the state: all under 65504 / 128 = 511.
 // Where m is infinite or NaN both are NaN, and so is then every state row: scaled by what is left of such a
 // bound, the rows without one in them would silently lose their bits.
 __device__ __forceinline__ float2 state_scale(float m) {
@@ -323,9 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = 16 * q4 + (lane >> 2);   // this thread's tokens of D1 and O: row, row + 8
     const int col = 2 * (lane & 3);          // its columns of them: 8 b + col, 8 b + col + 1, b = 0 .. 3
     const int n = 32 * q4 + lane;            // state column of this thread
-    // swizzled places: unit k of the thread's row of the S operand at s_at ^ 16 k, columns 8 b of its rows of V and R
-    // at r_at ^ 16 b
+    // swizzled places: unit k of the thread's row of the S operand at s_at ^ 16 k, columns 8 b of its rows of V and
+    // of y's R at r_at ^ 16 b, of R at w_at ^ 16 b (hi), w_at ^ 16 (4 + b) (lo)
     const uint32_t s_at = OFF_SB + hf * kHalf + swz(n, 0), r_at = swz(row, 4 * hf) + 2 * col;
+    const uint32_t w_at = OFF_SB + hf * kHalf + swz(row, 0) + 2 * col;
     uint32_t *max_s = reinterpret_cast<uint32_t *>(smem + OFF_MAXS) + 12 * hf;
     const uint32_t t_d1 = tmem + TM_D1 + 64 * hf, t_s = tmem + TM_S + 32 * hf;
     float2 S[16];  // the state, times sc.x
@@ -335,41 +345,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(fabsf(S[i].x), fabsf(S[i].y)));
       const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-      if (lane == 0) max_s[4 * buf + q4] = bits;
+      if (lead) {
+        max_s[4 * buf + q4] = bits;
+        mbar_arrive(BAR(BAR_MAX + hf));
+      }
+      __syncwarp();
     };
     const auto read_max = [&](int buf) {
       const uint4 a = *reinterpret_cast<const uint4 *>(max_s + 4 * buf);
       return __uint_as_float(max(max(a.x, a.y), max(a.z, a.w)));
     };
-    float m;    // bounds the state as described at state_scale
     float2 sc;
     uint32_t v[2][4];                  // the chunk's V, pairs
-    float gamma[2], beta[2], rho_k[2], gamma_end = 0.f, vmax = 0.f;  // of the chunk
+    float gr[2], u[2], w[2];           // of the chunk: 2^cs rho_k, u, w
+    float4 bound = make_float4(0.f, 0.f, 0.f, 0.f);  // 4 max |w V|, max |u V|, the first 2^cs, the last
     Ring<kDeep> ring;  // of the rows to load next
     const auto load_rows = [&](int c) {
       const unsigned char *stage = smem + OFF_VG + ring.at * kVG;
       const auto arr = [&](uint32_t off) { return reinterpret_cast<const float *>(stage + off); };
       const bool ok = wait(BAR_READY + ring.at, ring.parity);
-      vmax = reinterpret_cast<const float *>(smem + OFF_MAXV)[ring.at];
-      gamma_end = arr(OFF_GAMMA)[C - 1];
+      bound = reinterpret_cast<const float4 *>(smem + OFF_BOUND)[ring.at];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int t = row + 8 * i;
         const bool live = c * C + t < len;  // (the rows after may hold anything)
-        gamma[i] = arr(OFF_GAMMA)[t];
-        beta[i] = live ? arr(OFF_BETA)[t] : 0.f;
-        rho_k[i] = reinterpret_cast<const float *>(smem + ring.at * kTile + OFF_RHOK)[t];
+        gr[i] = arr(OFF_GAMMA)[t] * reinterpret_cast<const float *>(smem + ring.at * kTile + OFF_RHOK)[t];
+        u[i] = arr(OFF_U)[t];
+        w[i] = arr(OFF_W)[t];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const uint32_t u = *reinterpret_cast<const uint32_t *>(stage + (r_at ^ 16 * b) + 1024 * i);
-          v[i][b] = live ? u : 0u;
+          const uint32_t x = *reinterpret_cast<const uint32_t *>(stage + (r_at ^ 16 * b) + 1024 * i);
+          v[i][b] = live ? x : 0u;
         }
       }
       ring.next();
       return ok;
     };
     bool ok = true;
-    int k = 0, fulls = 0;  // chunks; items with chunks and an initial state
+    int k = 0, maxes = 0;  // chunks; largest |S| exchanged
     int seq = 0, hp_next = 0;  // of the next item
     for (uint32_t i = blockIdx.x; i < n_items + step && ok; i += step) {
       const int seq_now = seq, hp = hp_next;
@@ -395,12 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; ++j) p.h_final[soff + j * kDState] = j & 1 ? S[j / 2].y : S[j / 2].x;
         continue;
       }
-      m = 0.f;
+      float m = 0.f;
       if (p.h0) {
         publish_max(2);
-        if (lead) mbar_arrive(BAR(BAR_MAX + hf));
-        ok = wait(BAR_MAX + hf, fulls++ & 1);
-        __syncwarp();
+        ok = wait(BAR_MAX + hf, maxes++ & 1);
         m = read_max(2);
       }
       sc = state_scale(m);
@@ -428,14 +439,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; ++j) dst[j * kDState] = sc.y * (j & 1 ? S[j / 2].y : S[j / 2].x);
         }
         if (c == nck) break;
-        // while K S^T runs: the bound of |S|
+        // while K S^T runs: the largest |S|, and from it the scales of the next S (and R) and of y's R
         publish_max(k & 1);
-        const float2 rsc = state_scale(max_bound(m, vmax));
+        ok = wait(BAR_MAX + hf, maxes++ & 1) && ok;
+        // (A decay below 2^-126 is zero in 2^{cs_C}, but not yet in w_j 2^{cs_j}: it counts as that in the bound.  And S
+        // grows by at most 2^66 in its new scale, where zeros could otherwise meet an infinity.)
+        const float top = read_max(k & 1), decay = bound.w * sc.y, least = fmaxf(bound.w, 0x1p-126f) * sc.y;
+        const float2 nsc = state_scale(max_bound(fmaf(least, top, bound.x), 0x1p-60f * least));
+        const float2 ysc = state_scale(max_bound(bound.z * sc.y * top, bound.y));
         ok = wait(BAR_D1, k & 1) && ok;
         __syncwarp();
         tc_fence_after();
         // (for y; the place is free: the product was issued after the y of two chunks before)
-        if (q4 == 0 && lead) reinterpret_cast<float2 *>(smem + OFF_SCALE)[2 * hf + (k & 1)] = make_float2(sc.y, rsc.y);
+        if (q4 == 0 && lead) reinterpret_cast<float2 *>(smem + OFF_SCALE)[2 * hf + (k & 1)] = make_float2(sc.y, ysc.y);
         {
           float d[16], e[16];
           tmem_ld_rows(t_d1 + lane_off, d);
@@ -443,18 +459,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float g = -gamma[i] * sc.y * rho_k[i], bt = beta[i] * rsc.x;
-            const float2 k2 = make_float2(g, g), b2 = make_float2(bt, bt);
+            const float g = -gr[i] * sc.y, wn = w[i] * nsc.x, un = u[i] * ysc.x;
+            const float2 k2 = make_float2(g, g), w2 = make_float2(wn, wn), u2 = make_float2(un, un);
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
               const int x = 4 * b + 2 * i;
               const float2 vp = make_float2(__uint_as_float(v[i][b] << 16), __uint_as_float(v[i][b] & 0xffff0000u));
               const float2 ks = __fadd2_rn(make_float2(d[x], d[x + 1]), make_float2(e[x], e[x + 1]));
+              const float2 xv = __ffma2_rn(k2, ks, vp);
               uint32_t hv, lv;
-              split2(__fmul2_rn(b2, __ffma2_rn(k2, ks, vp)), hv, lv);
-              unsigned char *o = smem + OFF_R + (r_at ^ 16 * b) + 1024 * i;
-              *reinterpret_cast<uint32_t *>(o) = hv;
-              *reinterpret_cast<uint32_t *>(o + 8192) = lv;
+              split2(__fmul2_rn(w2, xv), hv, lv);
+              *reinterpret_cast<uint32_t *>(smem + (w_at ^ 16 * b) + 1024 * i) = hv;
+              *reinterpret_cast<uint32_t *>(smem + (w_at ^ 16 * (4 + b)) + 1024 * i) = lv;
+              *reinterpret_cast<uint32_t *>(smem + OFF_R + (r_at ^ 16 * b) + 1024 * i) = h2(__float22half2_rn(__fmul2_rn(u2, xv)));
             }
           }
         }
@@ -462,46 +479,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lead) mbar_arrive(BAR(BAR_RREADY + hf));
-        // S = gamma_end S + M R, in the next chunk's scale; while the product runs: the next chunk's rows
-        const float decay = gamma_end * sc.y, bound = vmax;
+        // S = gamma_end S + M R, in the new scale; while the product runs: the next chunk's rows
+        const float ge = decay * nsc.x;
+        const float2 ge2 = make_float2(ge, ge);
+        sc = nsc;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[i] = __fmul2_rn(S[i], ge2);
         if (c + 1 < nck) ok = load_rows(c + 1) && ok;
         ok = wait(BAR_S + hf, k & 1) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        // (not so far below the scale of R that the factor between the two overflows: a decay of the state to
-        // zero in a chunk without values)
-        m = max_bound(fmaf(decay, read_max(k & 1), bound), 0x1p-90f * 64.f * rsc.y);
-        sc = state_scale(m);
-        const float ge = decay * sc.x, yn = rsc.y * sc.x;
-        const float2 ge2 = make_float2(ge, ge), y2 = make_float2(yn, yn);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) S[i] = __fmul2_rn(S[i], ge2);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           float d[16];
           tmem_ld16(t_s + 16 * x + lane_off, d);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) S[8 * x + i] = __ffma2_rn(y2, make_float2(d[2 * i], d[2 * i + 1]), S[8 * x + i]);
+          for (int i = 0; i < 8; ++i) S[8 * x + i] = __fadd2_rn(make_float2(d[2 * i], d[2 * i + 1]), S[8 * x + i]);
         }
       }
     }
   } else if (warp < 12) {
-    // ------------------------------------------------------------------ M, its columns times
-    // rho_j 2^{cs_C - cs_j}, into its operand, a chunk ahead; y
+    // ------------------------------------------------------------------ M into its operand, a chunk ahead; y
     const int row = 16 * q4 + (lane >> 2), col = 2 * (lane & 3);  // tokens and columns as the chains'
     uint32_t total = 0;  // chunks of all items
     for (uint32_t i = blockIdx.x + lane * step; i < n_items; i += 32 * step) total += chunks_of(i);
     total = __reduce_add_sync(0xffffffffu, total);
-    Ring<kDeep> r, ry;  // of the chunk whose M is next; of the one whose y is
+    Ring<kDeep> ry;
     bool ok = true;
     const auto convert = [&](uint32_t k) {
-      ok = wait(BAR_VG + r.at, r.parity) && ok;  // the factors
       ok = wait2(BAR_M, k) && ok;
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      const float4 *f = reinterpret_cast<const float4 *>(smem + OFF_VG + r.at * kVG + OFF_END);
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {  // 16 tokens
         const uint32_t at = tmem + TM_M + 128 * (k & 1) + lane_off;
@@ -511,12 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16(at + 64 + 16 * b, e);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 x = f[4 * b + j];
-          const auto sum = [&](int i) { return __fadd2_rn(make_float2(m[i], m[i + 1]), make_float2(e[i], e[i + 1])); };
-          split2(__fmul2_rn(sum(4 * j), make_float2(x.x, x.y)), hv[2 * j], lv[2 * j]);
-          split2(__fmul2_rn(sum(4 * j + 2), make_float2(x.z, x.w)), hv[2 * j + 1], lv[2 * j + 1]);
-        }
+        for (int j = 0; j < 8; ++j)
+          split2(__fadd2_rn(make_float2(m[2 * j], m[2 * j + 1]), make_float2(e[2 * j], e[2 * j + 1])), hv[j], lv[j]);
         tmem_st8(at + 16 * b, hv);
         tmem_st8(at + 16 * b + 8, lv);
       }
@@ -524,7 +530,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lead) mbar_arrive(BAR(BAR_MREADY + (k & 1)));
-      r.next();
     };
     uint32_t k = 0;
     if (total > 0) convert(0);
@@ -560,7 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               hold[hf][t][b] = __fadd2_rn(make_float2(d[x], d[x + 1]), make_float2(e[x], e[x + 1]));
             }
         }
-        ok = wait(BAR_TILE + ry.at, ry.parity) && ok;  // (done: what it loaded is read here)
+        ok = wait(BAR_TILE + ry.at, ry.parity) && ok;  // (done: what they loaded is read here)
+        ok = wait(BAR_VG + ry.at, ry.parity) && ok;
         float gamma[2], rho[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -627,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int half = 0; half < 2; ++half) {
           ok = wait(BAR_RREADY + half, k & 1) && ok;
           tc_fence_after();
-          issue_S(tmem + TM_M + 128 * (k & 1), sb + OFF_R, half, tmem + TM_S + 32 * half);
+          issue_S(tmem + TM_M + 128 * (k & 1), sb + OFF_SB + half * kHalf, tmem + TM_S + 32 * half);
           commit(BAR(BAR_S + half));
         }
         ok = wait2(BAR_AT, k) && ok;
@@ -706,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
           mbar_arrive_expect_tx(tb, (uint32_t)kDeltaTileBytes);
           bulk_load(sb + r.at * kTile, tile, (uint32_t)kDeltaTileBytes, tb);
-          bulk_load(dst + OFF_BETA, rec + kDeltaATBytes, 768, vg);
+          bulk_load(dst + OFF_U, rec + kDeltaATBytes, 768, vg);
           r.next();
           if (n != 1) load_at(n == 0 ? rec : before);
           before = rec;
@@ -725,8 +731,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------------ loads of T; the largest |V| of each chunk,
-    // times the largest |beta| / 2 where that is above one
+    // ------------------------------------------------------------------ loads of T; the bounds of what each chunk
+    // adds to the state and to y
     uint32_t i = blockIdx.x - step;  // the item of the T to load, its chunks, the chunk
     int len = 0, nck = 0, c = 0;
     const unsigned char *rec = nullptr;
@@ -748,18 +754,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = wait(BAR_VG + r.at, r.parity);
         ok = wait(BAR_TILE + r.at, r.parity) && ok;
         const unsigned char *stage = smem + OFF_VG + r.at * kVG;
-        uint32_t top = 0;
+        const float *u = reinterpret_cast<const float *>(stage + OFF_U), *w = reinterpret_cast<const float *>(stage + OFF_W);
+        uint32_t top_w = 0, top_u = 0;
 #pragma unroll 4
         for (int t = lane >> 3; t < rows; t += 4) {
-          const uint4 u = *reinterpret_cast<const uint4 *>(stage + t * 128 + (lane & 7) * 16);
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
-                                       __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+          const uint4 x = *reinterpret_cast<const uint4 *>(stage + t * 128 + (lane & 7) * 16);
+          const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+          // at least 2^-100, so that u and w times a scale are finite (as integers, where a NaN ranks highest)
+          const float v = __uint_as_float(max(max(m << 16, m & 0x7fff0000u), 0x0d800000u));
+          top_w = max(top_w, __float_as_uint(fabsf(w[t] * v)));
+          top_u = max(top_u, __float_as_uint(fabsf(u[t] * v)));
         }
-        top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-        const float2 b = reinterpret_cast<const float2 *>(stage + OFF_BETA)[lane];
-        const uint32_t bt = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(b.x), fabsf(b.y))));
+        top_w = __reduce_max_sync(0xffffffffu, top_w);
+        top_u = __reduce_max_sync(0xffffffffu, top_u);
         if (lead) {
-          reinterpret_cast<float *>(smem + OFF_MAXV)[r.at] = __uint_as_float(top << 16) * fmaxf(1.f, 0.5f * __uint_as_float(bt));
+          const float *gamma = reinterpret_cast<const float *>(stage + OFF_GAMMA);
+          reinterpret_cast<float4 *>(smem + OFF_BOUND)[r.at] =
+              make_float4(4.f * __uint_as_float(top_w), __uint_as_float(top_u), gamma[0], gamma[C - 1]);
           mbar_arrive(BAR(BAR_READY + r.at));
         }
         __syncwarp();
