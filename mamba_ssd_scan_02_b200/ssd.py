@@ -524,23 +524,38 @@ def _rows(t, name, dtype, device, shape):
     return t.data_ptr(), st[many[-1]]
 
 
-def _call(fn, where, device, stream, made, *args):
-    """Runs fn(*args, stream) with `device` current.  `stream` None: the device's current stream.
-    Tensors in `made` were allocated here, under the current stream: on another one, the
-    allocator is told so."""
+def _other_stream(stream, device, where):
+    """`stream` (a torch stream or a handle) where it is not the device's current stream, else None."""
     import torch
     if device.type != "cuda":
         raise ValueError(f"{where}: tensors must be on a CUDA device, got {device}")
-    if stream is None:  # (torch.cuda.current_stream would cost 2 us, as much as the launch)
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
-    else:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        if stream.device != device:
-            raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {device}")
-        handle = stream.cuda_stream
-        for t in made:
-            t.record_stream(stream)
+    if stream is None:
+        return None
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {device}")
+    return None if stream.cuda_stream == torch._C._cuda_getCurrentRawStream(device.index) else stream
+
+
+def _made(other, make):
+    """make(), tensors for a call on the stream `other` (None: the current one).  They come from that stream's
+    memory, so that nothing still queued on the current stream writes them, and a fill is in order with the
+    call; the current stream, on which the caller may use them, is recorded."""
+    if other is None:
+        return make()
+    import torch
+    with torch.cuda.stream(other):
+        t = make()
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _call(fn, where, device, other, *args):
+    """Runs fn(*args, stream) with `device` current, on the stream `other`, or None: the device's current one."""
+    import torch
+    # (torch.cuda.current_stream would cost 2 us, as much as the launch)
+    handle = torch._C._cuda_getCurrentRawStream(device.index) if other is None else other.cuda_stream
     if torch.cuda.current_device() == device.index:
         status = fn(*args, handle)
     else:
@@ -573,29 +588,26 @@ def _delta_prefill(cfg, c, cu, nseq, lead, q, k, v, dt, b, A, dt_bias, h0, y, h_
             *_rows(dt, "dt", dtype, dev, heads), *_rows(b, "b", dtype, dev, heads),
             _check_dense(A, "A", f32, dev, (H,)), _check_dense(dt_bias, "dt_bias", f32, dev, (H,)),
             None if h0 is None else _check_dense(h0, "h0", f32, dev, states))
-    made = []
+    where = "ssd_delta_prefill" if cu is None else "ssd_delta_prefill_varlen"
+    other = _other_stream(stream, dev, where)
     if y is None:
-        y = v.new_empty(wide)
-        made.append(y)
+        y = _made(other, lambda: v.new_empty(wide))
     if h_final is None and want_state:
-        h_final = A.new_empty(states)
-        made.append(h_final)
+        h_final = _made(other, lambda: A.new_empty(states))
     if workspace is None:
         n = (lib.ssd_delta_varlen_workspace_size(ctypes.byref(c), cu, nseq) if cu is not None
              else lib.ssd_delta_workspace_size(ctypes.byref(c)))
         if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-            made.append(workspace)
+            workspace = _made(other, lambda: torch.empty(n, dtype=torch.uint8, device=dev))
     args = DeltaArgs(
         *rows, *_rows(y, "y", dtype, dev, wide),
         None if h_final is None else _check_dense(h_final, "h_final", f32, dev, states),
         None if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.numel() * workspace.element_size())
     if cu is None:
-        _call(lib.ssd_delta_prefill, "ssd_delta_prefill", dev, stream, made, ctypes.byref(c), ctypes.byref(args))
+        _call(lib.ssd_delta_prefill, where, dev, other, ctypes.byref(c), ctypes.byref(args))
     else:
-        _call(lib.ssd_delta_prefill_varlen, "ssd_delta_prefill_varlen", dev, stream, made,
-              ctypes.byref(c), ctypes.byref(args), cu, nseq)
+        _call(lib.ssd_delta_prefill_varlen, where, dev, other, ctypes.byref(c), ctypes.byref(args), cu, nseq)
     return y, h_final
 
 
@@ -603,7 +615,9 @@ def delta_prefill(cfg: dict, q, k, v, dt, b, A, dt_bias, h0=None, *, y=None, h_f
                   workspace=None, stream=None, want_state: bool = True, kernel: int | None = None):
     """ssd_delta_prefill: the gated delta rule over q, k [B, L, G*N], v [B, L, H*P] and the raw gates
     dt, b [B, L, H] (see make_delta_config for cfg), from the state h0 [B, H, P, N]; returns
-    (y [B, L, H*P], h_final [B, H, P, N], or None when want_state is False)."""
+    (y [B, L, H*P], h_final [B, H, P, N], or None when want_state is False).  On a `stream` that is not the
+    current one the call waits for nothing on the current stream: inputs made there are the caller's to wait
+    for, as the outputs are afterwards (the same holds for the calls below)."""
     if q.dim() != 3:
         raise ValueError(f"q must be [batch, seqlen, ngroups * dstate], got {tuple(q.shape)}")
     Bn, L = q.shape[0], q.shape[1]
@@ -640,19 +654,17 @@ def delta_decode_step(cfg: dict, q_t, k_t, v_t, dt_t, b_t, A, dt_bias, state, sl
     c = make_delta_config(cfg, Bn, 1)
     H, P, N, G = c.nheads, c.headdim, c.dstate, c.ngroups
     dev, dtype, f32 = q_t.device, io_dtype(cfg), torch.float32
-    made = []
+    rows = (*_rows(q_t, "q_t", dtype, dev, (Bn, G * N)), *_rows(k_t, "k_t", dtype, dev, (Bn, G * N)),
+            *_rows(v_t, "v_t", dtype, dev, (Bn, H * P)), *_rows(dt_t, "dt_t", dtype, dev, (Bn, H)),
+            *_rows(b_t, "b_t", dtype, dev, (Bn, H)), _check_dense(A, "A", f32, dev, (H,)),
+            _check_dense(dt_bias, "dt_bias", f32, dev, (H,)),
+            _check_dense(state, "state", f32, dev, (state.shape[0], H, P, N)),
+            None if slots is None else _check_dense(slots, "slots", torch.int32, dev, (Bn,)), state.shape[0])
+    other = _other_stream(stream, dev, "ssd_delta_decode_step")
     if y is None:
-        y = (torch.empty if slots is None else torch.zeros)((Bn, H * P), dtype=dtype, device=dev)
-        made.append(y)
-    a = DeltaDecodeArgs(
-        *_rows(q_t, "q_t", dtype, dev, (Bn, G * N)), *_rows(k_t, "k_t", dtype, dev, (Bn, G * N)),
-        *_rows(v_t, "v_t", dtype, dev, (Bn, H * P)), *_rows(dt_t, "dt_t", dtype, dev, (Bn, H)),
-        *_rows(b_t, "b_t", dtype, dev, (Bn, H)), _check_dense(A, "A", f32, dev, (H,)),
-        _check_dense(dt_bias, "dt_bias", f32, dev, (H,)),
-        _check_dense(state, "state", f32, dev, (state.shape[0], H, P, N)),
-        None if slots is None else _check_dense(slots, "slots", torch.int32, dev, (Bn,)),
-        state.shape[0], *_rows(y, "y", dtype, dev, (Bn, H * P)))
-    _call(lib.ssd_delta_decode_step, "ssd_delta_decode_step", dev, stream, made, ctypes.byref(c), ctypes.byref(a))
+        y = _made(other, lambda: (torch.empty if slots is None else torch.zeros)((Bn, H * P), dtype=dtype, device=dev))
+    a = DeltaDecodeArgs(*rows, *_rows(y, "y", dtype, dev, (Bn, H * P)))
+    _call(lib.ssd_delta_decode_step, "ssd_delta_decode_step", dev, other, ctypes.byref(c), ctypes.byref(a))
     return y
 
 
@@ -694,7 +706,7 @@ def _state_cache_call(name, states, cache, scales, state_slots, cache_slots, str
         None if state_slots is None else _check_dense(state_slots, "state_slots", torch.int32, dev, (count,)),
         None if cache_slots is None else _check_dense(cache_slots, "cache_slots", torch.int32, dev, (count,)),
         n, places, ps, pc, pf)
-    _call(getattr(load(), name), name, dev, stream, (), ctypes.byref(a))
+    _call(getattr(load(), name), name, dev, _other_stream(stream, dev, name), ctypes.byref(a))
 
 
 def state_store(states, cache, scales, state_slots=None, cache_slots=None, *, stream=None):
