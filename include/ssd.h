@@ -256,7 +256,9 @@ typedef struct {
   ssd_dtype_t io_dtype; /* dtype of q, k, v, dt, b and y */
   ssd_kernel_t kernel;  /* TENSOR: the chunked kernels (bf16 only; UNSUPPORTED otherwise); SIMT: the
                            recurrence in fp32; AUTO: whichever is faster for the lengths, the chunked
-                           ones only with qk_norm, beta_sigmoid and beta_scale in [0, 2] */
+                           ones only with qk_norm, beta_sigmoid, beta_scale in [0, 2] and a dt that cannot
+                           be negative (dt_min >= 0, or dt_softplus with dt_max >= 0); it takes A <= 0 for
+                           granted */
 } ssd_delta_config_t;
 
 typedef struct {

@@ -87,8 +87,10 @@ bool packed(const ssd_delta_config_t *c, const int *cu, int nseq, Batch *b) {
 bool uses_chunks(const ssd_delta_config_t *c, const Batch &b) {
   if (b.rows == 0 || c->kernel == SSD_KERNEL_SIMT) return false;
   if (c->kernel == SSD_KERNEL_TENSOR) return true;
-  // Their operands are bounded where beta |k|^2 is, by 2; AUTO takes them where the configuration says so.
-  const bool bounded = c->qk_norm && c->beta_sigmoid && c->beta_scale >= 0.f && c->beta_scale <= 2.f;
+  // Their operands are bounded where beta |k|^2 is, by 2, and alpha, by 1; AUTO takes them where the configuration says
+  // so.  (That A <= 0 is taken for granted: it is on the device.)
+  const bool steps = c->dt_min >= 0.f || (c->dt_softplus && c->dt_max >= 0.f);  // dt >= 0
+  const bool bounded = steps && c->qk_norm && c->beta_sigmoid && c->beta_scale >= 0.f && c->beta_scale <= 2.f;
   const bool one_each = (long long)b.nseq * c->nheads * c->headdim <= 16 * 148;
   return c->io_dtype == SSD_BF16 && bounded && b.longest >= (one_each ? 128 : 28) && tc_scan_available();
 }
