@@ -269,12 +269,13 @@ typedef struct {
   const void *b;  long long b_row_stride;   /* [B, L, H] raw beta */
   const float *A, *dt_bias;                 /* [H] */
   const float *h0;      /* [B, H, P, N] initial state or NULL (= 0) */
-  void *y;  long long y_row_stride;         /* [B, L, H*P] output; must not overlap an input */
-  float *h_final;       /* [B, H, P, N] state after the last token, or NULL; may be h0 itself, but
-                           must not overlap it in part */
+  void *y;  long long y_row_stride;         /* [B, L, H*P] output.  Columns of a matrix that other of its
+                           columns are inputs of are fine */
+  float *h_final;       /* [B, H, P, N] state after the last token, or NULL; may be h0 itself */
   void *workspace;      /* at least ssd_delta_workspace_size() bytes, 256-B aligned (NULL if 0) */
   size_t workspace_bytes;
-} ssd_delta_args_t;
+} ssd_delta_args_t;     /* y, h_final and the workspace overlap nothing else, but h_final = h0
+                           (SSD_ERR_INVALID_ARG) */
 
 typedef struct {
   const void *q;  long long q_row_stride;   /* [B, G*N] */
@@ -290,7 +291,7 @@ typedef struct {
                            skipped too and latches SSD_ERR_DEVICE_BOUNDS. */
   int n_slots;          /* states in the pool (>= B when slots is NULL) */
   void *y;  long long y_row_stride;         /* [B, H*P] output */
-} ssd_delta_decode_args_t;
+} ssd_delta_decode_args_t;  /* y and the states overlap nothing else (SSD_ERR_INVALID_ARG) */
 
 /* Bytes of scratch ssd_delta_prefill needs (0 if the config is invalid, or nothing is needed). */
 size_t ssd_delta_workspace_size(const ssd_delta_config_t *cfg);
@@ -335,7 +336,7 @@ ssd_status_t ssd_delta_decode_step(const ssd_delta_config_t *cfg, const ssd_delt
  * entry i of ssd_state_load writes cache slot cache_slots[i] to states[state_slots[i]].  An entry
  * with a negative slot on either side is skipped.  A slot outside its array, or a destination that
  * an earlier entry has, is skipped too and latches SSD_ERR_DEVICE_BOUNDS.  state_elems is a
- * multiple of 128.  The destination must not overlap the source. */
+ * multiple of 128.  States, cache and scales overlap nowhere, and the destination no slots. */
 typedef enum { SSD_STATE_E4M3 = 0, SSD_STATE_INT8 = 1 } ssd_state_format_t;
 
 typedef struct {

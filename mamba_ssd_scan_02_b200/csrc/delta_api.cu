@@ -26,16 +26,34 @@ bool ranges_overlap(const void *a, size_t na, const void *b, size_t nb) {
   return na && nb && pa < pb + nb && pb < pa + na;
 }
 
-// Whether two sets of n rows (wa, wb bytes wide, sa, sb bytes apart) share a byte.  Rows of equal
-// stride may interleave (columns of one matrix); of different strides, overlapping spans count.
-bool rows_overlap(const void *a, long long sa, long long wa, const void *b, long long sb, long long wb, long long n) {
-  if (!a || !b || n < 1) return false;
-  if (!ranges_overlap(a, (size_t)((n - 1) * sa + wa), b, (size_t)((n - 1) * sb + wb))) return false;
-  if (n > 1 && sa != sb) return true;
-  if (n == 1) return true;
-  long long d = (long long)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)) % sa;
-  if (d < 0) d += sa;
-  return d < wa || d + wb > sa;
+// n rows of `width` bytes, `stride` bytes apart
+struct Rows {
+  const void *p;
+  long long stride, width, n;
+};
+Rows dense(const void *p, long long bytes) { return Rows{p, bytes, bytes, 1}; }
+
+// Whether two sets of rows share a byte.  Rows of equal stride may interleave (columns of one matrix); of different
+// strides, overlapping spans count.
+bool overlap(const Rows &a, const Rows &b) {
+  if (!a.p || !b.p || a.n < 1 || b.n < 1 || a.width < 1 || b.width < 1) return false;
+  if (!ranges_overlap(a.p, (size_t)((a.n - 1) * a.stride + a.width), b.p, (size_t)((b.n - 1) * b.stride + b.width))) return false;
+  if (a.n == 1) {  // the first row of b that ends behind a's start, if it begins before a's end
+    const long long d = (long long)(reinterpret_cast<uintptr_t>(a.p) - reinterpret_cast<uintptr_t>(b.p));
+    const long long row = d < b.width ? 0 : (d - b.width) / b.stride + 1;
+    return row < b.n && row * b.stride < d + a.width;
+  }
+  if (b.n == 1) return overlap(b, a);
+  if (a.stride != b.stride) return true;
+  long long d = (long long)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % a.stride;
+  if (d < 0) d += a.stride;
+  return d < a.width || d + b.width > a.stride;
+}
+// Whether `out` shares a byte with one of the others
+bool overlaps_any(const Rows &out, const Rows *others, int n) {
+  for (int i = 0; i < n; ++i)
+    if (overlap(out, others[i])) return true;
+  return false;
 }
 
 ssd_status_t check_config(const ssd_delta_config_t *c) {
@@ -138,13 +156,26 @@ ssd_status_t check_rows(const ssd_delta_config_t *c, const Args *a, long long ro
     return SSD_ERR_ALIGNMENT;
   const uintptr_t es = c->io_dtype == SSD_F32 ? 4 : 2;
   if (!aligned(a->dt, es) || !aligned(a->b, es) || !aligned(a->A, 4) || !aligned(a->dt_bias, 4)) return SSD_ERR_ALIGNMENT;
-  const long long e = (long long)es, ys = a->y_row_stride * e;
-  const void *in[] = {a->q, a->k, a->v, a->dt, a->b};
-  const long long st[] = {a->q_row_stride, a->k_row_stride, a->v_row_stride, a->dt_row_stride, a->b_row_stride};
-  const long long wd[] = {qk, qk, w, c->nheads, c->nheads};
-  for (int i = 0; i < 5; ++i)
-    if (rows_overlap(a->y, ys, w * e, in[i], st[i] * e, wd[i] * e, rows)) return SSD_ERR_INVALID_ARG;
   return SSD_OK;
+}
+
+// What a call reads but the states and slots, and y
+constexpr int kInputs = 7;
+template <class Args>
+void input_rows(const ssd_delta_config_t *c, const Args *a, long long rows, Rows *in) {
+  const long long e = c->io_dtype == SSD_F32 ? 4 : 2, qk = c->ngroups * kDState * e, H = c->nheads;
+  in[0] = Rows{a->q, a->q_row_stride * e, qk, rows};
+  in[1] = Rows{a->k, a->k_row_stride * e, qk, rows};
+  in[2] = Rows{a->v, a->v_row_stride * e, H * c->headdim * e, rows};
+  in[3] = Rows{a->dt, a->dt_row_stride * e, H * e, rows};
+  in[4] = Rows{a->b, a->b_row_stride * e, H * e, rows};
+  in[5] = dense(rows > 0 ? a->A : nullptr, 4 * H);
+  in[6] = dense(rows > 0 ? a->dt_bias : nullptr, 4 * H);
+}
+template <class Args>
+Rows y_rows(const ssd_delta_config_t *c, const Args *a, long long rows) {
+  const long long e = c->io_dtype == SSD_F32 ? 4 : 2;
+  return Rows{a->y, a->y_row_stride * e, (long long)c->nheads * c->headdim * e, rows};
 }
 
 template <class Args>
@@ -162,13 +193,20 @@ ssd_status_t run_prefill(const ssd_delta_config_t *c, const ssd_delta_args_t *a,
     if (st != SSD_OK) return st;
   }
   if (!aligned(a->h0, 16) || !aligned(a->h_final, 16)) return SSD_ERR_ALIGNMENT;
-  const size_t state = (size_t)b.nseq * c->nheads * c->headdim * kDState * sizeof(float);
-  if (a->h0 && a->h_final && a->h0 != a->h_final && ranges_overlap(a->h0, state, a->h_final, state))
+  const long long state = (long long)b.nseq * c->nheads * c->headdim * kDState * (long long)sizeof(float);
+  Rows in[kInputs + 1];
+  input_rows(c, a, b.rows, in);
+  in[kInputs] = dense(a->h0, state);
+  const Rows y = y_rows(c, a, b.rows), h_final = dense(a->h_final, state);
+  if (overlaps_any(y, in, kInputs + 1) || overlap(y, h_final) || overlaps_any(h_final, in, kInputs) ||
+      (a->h0 != a->h_final && overlap(h_final, in[kInputs])))
     return SSD_ERR_INVALID_ARG;
   if ((long long)b.nseq * c->nheads * (c->headdim / 64) > 1 << 30) return SSD_ERR_UNSUPPORTED;
   const Layout l = layout(c, b);
   if (l.total && (!a->workspace || a->workspace_bytes < l.total || !aligned(a->workspace, kAlign)))
     return SSD_ERR_WORKSPACE;
+  const Rows scratch = dense(a->workspace, (long long)l.total);
+  if (overlaps_any(scratch, in, kInputs + 1) || overlap(scratch, y) || overlap(scratch, h_final)) return SSD_ERR_INVALID_ARG;
   if (b.rows == 0 && !a->h_final) return SSD_OK;
 
   DeltaPlan p{};
@@ -220,6 +258,13 @@ ssd_status_t run_decode(const ssd_delta_config_t *c, const ssd_delta_decode_args
   if ((st = check_rows(c, a, c->batch)) != SSD_OK) return st;
   if (a->n_slots < 1 || (!a->slots && a->n_slots < c->batch)) return SSD_ERR_INVALID_ARG;
   if (!aligned(a->state, 16) || !aligned(a->slots, 4)) return SSD_ERR_ALIGNMENT;
+  Rows in[kInputs];
+  input_rows(c, a, c->batch, in);
+  const Rows y = y_rows(c, a, c->batch), slots = dense(a->slots, 4LL * c->batch);
+  const Rows states = dense(a->state, (long long)a->n_slots * c->nheads * c->headdim * kDState * 4);
+  if (overlaps_any(y, in, kInputs) || overlap(y, slots) || overlap(y, states) || overlaps_any(states, in, kInputs) ||
+      overlap(states, slots))
+    return SSD_ERR_INVALID_ARG;
   DeltaPlan p{};
   fill(p, c);
   fill_rows(p, a);
@@ -241,10 +286,13 @@ ssd_status_t run_state_cache(const ssd_state_cache_args_t *a, bool store, cudaSt
   if (!aligned(a->states, 16) || !aligned(a->cache, 16) || !aligned(a->scales, 4) || !aligned(a->state_slots, 4) ||
       !aligned(a->cache_slots, 4))
     return SSD_ERR_ALIGNMENT;
-  const size_t n = (size_t)a->state_elems;
-  if (ranges_overlap(a->states, n * 4 * a->n_states, a->cache, n * a->n_cache) ||
-      ranges_overlap(a->states, n * 4 * a->n_states, a->scales, n / 32 * a->n_cache) ||
-      ranges_overlap(a->cache, n * a->n_cache, a->scales, n / 32 * a->n_cache))
+  // (below 2^62 bytes: sizes that no memory has would wrap around in the checks)
+  if (a->state_elems > (1LL << 60) / std::max(a->n_states, a->n_cache)) return SSD_ERR_UNSUPPORTED;
+  const Rows states = dense(a->states, 4 * a->state_elems * a->n_states), cache = dense(a->cache, a->state_elems * a->n_cache);
+  const Rows scales = dense(a->scales, a->state_elems / 32 * a->n_cache);
+  const Rows slots[] = {dense(a->state_slots, 4LL * a->count), dense(a->cache_slots, 4LL * a->count)};
+  if (overlap(states, cache) || overlap(states, scales) || overlap(cache, scales)) return SSD_ERR_INVALID_ARG;
+  if (store ? overlaps_any(cache, slots, 2) || overlaps_any(scales, slots, 2) : overlaps_any(states, slots, 2))
     return SSD_ERR_INVALID_ARG;
   StateCachePlan p{a->format, a->state_elems, a->count, a->n_states, a->n_cache, a->state_slots, a->cache_slots,
                    a->states, static_cast<unsigned char *>(a->cache), a->scales, device_error_ptr(),
