@@ -588,6 +588,8 @@ def _delta_prefill(cfg, c, cu, nseq, lead, q, k, v, dt, b, A, dt_bias, h0, y, h_
             *_rows(dt, "dt", dtype, dev, heads), *_rows(b, "b", dtype, dev, heads),
             _check_dense(A, "A", f32, dev, (H,)), _check_dense(dt_bias, "dt_bias", f32, dev, (H,)),
             None if h0 is None else _check_dense(h0, "h0", f32, dev, states))
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be contiguous on {dev}, got {tuple(workspace.shape)} on {workspace.device}")
     where = "ssd_delta_prefill" if cu is None else "ssd_delta_prefill_varlen"
     other = _other_stream(stream, dev, where)
     if y is None:
