@@ -570,9 +570,18 @@ def delta_workspace_size(cfg: dict, batch: int, seqlen: int, kernel: int | None 
     return load().ssd_delta_workspace_size(ctypes.byref(make_delta_config(cfg, batch, seqlen, kernel)))
 
 
+def _offsets(cu_seqlens):
+    cu = [int(v) for v in cu_seqlens]
+    if len(cu) < 2:
+        raise ValueError("cu_seqlens needs at least two offsets")
+    if any(v >> 31 for v in cu):  # (ctypes would take their low 32 bits)
+        raise ValueError("offsets must be in [0, 2^31)")
+    return cu
+
+
 def delta_varlen_workspace_size(cfg: dict, cu_seqlens, kernel: int | None = None) -> int:
     """ssd_delta_varlen_workspace_size for the packed batch with offsets cu_seqlens."""
-    cu = [int(v) for v in cu_seqlens]
+    cu = _offsets(cu_seqlens)
     c = make_delta_config(cfg, 1, cu[-1], kernel)
     return load().ssd_delta_varlen_workspace_size(ctypes.byref(c), (c_int * len(cu))(*cu), len(cu) - 1)
 
@@ -634,9 +643,7 @@ def delta_prefill_varlen(cfg: dict, cu_seqlens, q, k, v, dt, b, A, dt_bias, h0=N
     """ssd_delta_prefill_varlen: packed sequences (q, k [T, G*N], ... with T = cu_seqlens[-1], host
     offsets cu_seqlens), each from its own state h0[i]; returns (y [T, H*P], h_final
     [nseq, H, P, N], or None when want_state is False)."""
-    cu = [int(v_) for v_ in cu_seqlens]
-    if len(cu) < 2:
-        raise ValueError("cu_seqlens needs at least two offsets")
+    cu = _offsets(cu_seqlens)
     c = make_delta_config(cfg, 1, cu[-1], kernel)
     return _delta_prefill(cfg, c, (c_int * len(cu))(*cu), len(cu) - 1, (cu[-1],), q, k, v, dt, b, A,
                           dt_bias, h0, y, h_final, workspace, stream, want_state)

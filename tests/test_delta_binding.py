@@ -23,3 +23,12 @@ def test_workspace(workspace):
         ssd.delta_prefill(CFG, **tensors(), workspace=workspace)
     with pytest.raises(ValueError, match="workspace"):
         ssd.delta_prefill_varlen(CFG, [0, 4], **tensors((4,)), workspace=workspace)
+
+
+@pytest.mark.parametrize("cu", [[0, (1 << 32) + 2, 4], [1 << 32, 4], [0, (1 << 32) + 4], [0, 2 - (1 << 32), 4], [0, -1, 4]], ids=str)
+def test_offsets_beyond_32_bits(cu):
+    """Not taken as their low 32 bits, which here would make a valid batch."""
+    with pytest.raises(ValueError, match="offsets"):
+        ssd.delta_prefill_varlen(CFG, cu, **tensors((4,)))
+    with pytest.raises(ValueError, match="offsets"):
+        ssd.delta_varlen_workspace_size(CFG, cu)
