@@ -101,7 +101,10 @@ bool packed(const ssd_delta_config_t *c, const int *cu, int nseq, Batch *b) {
 // The longest sequence from which AUTO takes the chunked kernels.  They cost two launches and a chunk's latency
 // (15 us); the recurrence costs its longest sequence, times its CTAs per SM once the state rows are more than
 // one CTA per SM holds.  Both in us, bf16, at 64, 96, 128 tokens: 8 heads of 64 rows 9.3 : 15.0, 12.4 : 16.5,
-// 15.6 : 16.6; at 16, 32, 64 tokens: 4 sequences of 32 heads 11.6 : 16.8, 18.4 : 16.9, 31.7 : 17.1.
+// 15.6 : 16.6; at 16, 32, 64 tokens: 4 sequences of 32 heads 11.6 : 16.8, 18.4 : 16.9, 31.7 : 17.1.  Short sequences
+// beside the longest change little, since a state in and out is most of what either costs them: 63 of one token
+// and one of 28 tokens, 128 heads 387 : 324, 32 heads 94.5 : 97.3; 255 and one, 128 heads 1503 : 1212; 7 and one, 32
+// heads 18.6 : 24.7, the most that the rule loses.
 bool uses_chunks(const ssd_delta_config_t *c, const Batch &b) {
   if (b.rows == 0 || c->kernel == SSD_KERNEL_SIMT) return false;
   if (c->kernel == SSD_KERNEL_TENSOR) return true;

@@ -525,12 +525,10 @@ def _rows(t, name, dtype, device, shape):
 
 
 def _other_stream(stream, device, where):
-    """`stream` (a torch stream or a handle) where it is not the device's current stream, else None."""
-    import torch
-    if device.type != "cuda":
-        raise ValueError(f"{where}: tensors must be on a CUDA device, got {device}")
-    if stream is None:
+    """`stream` (a torch stream, a handle, or None) where it is not the device's current stream, else None."""
+    if stream is None or device.type != "cuda":
         return None
+    import torch
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     if stream.device != device:
@@ -538,15 +536,15 @@ def _other_stream(stream, device, where):
     return None if stream.cuda_stream == torch._C._cuda_getCurrentRawStream(device.index) else stream
 
 
-def _made(other, make):
-    """make(), tensors for a call on the stream `other` (None: the current one).  They come from that stream's
-    memory, so that nothing still queued on the current stream writes them, and a fill is in order with the
-    call; the current stream, on which the caller may use them, is recorded."""
+def _made(other, make, *args, **kw):
+    """make(*args, **kw), a tensor for a call on the stream `other` (None: the current one).  It comes from that
+    stream's memory, so that nothing still queued on the current stream writes it, and a fill is in order with
+    the call; the current stream, on which the caller may use it, is recorded."""
     if other is None:
-        return make()
+        return make(*args, **kw)
     import torch
     with torch.cuda.stream(other):
-        t = make()
+        t = make(*args, **kw)
     t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
@@ -554,6 +552,8 @@ def _made(other, make):
 def _call(fn, where, device, other, *args):
     """Runs fn(*args, stream) with `device` current, on the stream `other`, or None: the device's current one."""
     import torch
+    if device.type != "cuda":
+        raise ValueError(f"{where}: tensors must be on a CUDA device, got {device}")
     # (torch.cuda.current_stream would cost 2 us, as much as the launch)
     handle = torch._C._cuda_getCurrentRawStream(device.index) if other is None else other.cuda_stream
     if torch.cuda.current_device() == device.index:
@@ -574,7 +574,7 @@ def _offsets(cu_seqlens):
     cu = [int(v) for v in cu_seqlens]
     if len(cu) < 2:
         raise ValueError("cu_seqlens needs at least two offsets")
-    if any(v >> 31 for v in cu):  # (ctypes would take their low 32 bits)
+    if min(cu) < 0 or max(cu) >> 31:  # (ctypes would take their low 32 bits)
         raise ValueError("offsets must be in [0, 2^31)")
     return cu
 
@@ -600,16 +600,16 @@ def _delta_prefill(cfg, c, cu, nseq, lead, q, k, v, dt, b, A, dt_bias, h0, y, h_
     if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be contiguous on {dev}, got {tuple(workspace.shape)} on {workspace.device}")
     where = "ssd_delta_prefill" if cu is None else "ssd_delta_prefill_varlen"
-    other = _other_stream(stream, dev, where)
+    other = None if stream is None else _other_stream(stream, dev, where)
     if y is None:
-        y = _made(other, lambda: v.new_empty(wide))
+        y = _made(other, v.new_empty, wide)
     if h_final is None and want_state:
-        h_final = _made(other, lambda: A.new_empty(states))
+        h_final = _made(other, A.new_empty, states)
     if workspace is None:
         n = (lib.ssd_delta_varlen_workspace_size(ctypes.byref(c), cu, nseq) if cu is not None
              else lib.ssd_delta_workspace_size(ctypes.byref(c)))
         if n:
-            workspace = _made(other, lambda: torch.empty(n, dtype=torch.uint8, device=dev))
+            workspace = _made(other, torch.empty, n, dtype=torch.uint8, device=dev)
     args = DeltaArgs(
         *rows, *_rows(y, "y", dtype, dev, wide),
         None if h_final is None else _check_dense(h_final, "h_final", f32, dev, states),
@@ -669,9 +669,9 @@ def delta_decode_step(cfg: dict, q_t, k_t, v_t, dt_t, b_t, A, dt_bias, state, sl
             _check_dense(dt_bias, "dt_bias", f32, dev, (H,)),
             _check_dense(state, "state", f32, dev, (state.shape[0], H, P, N)),
             None if slots is None else _check_dense(slots, "slots", torch.int32, dev, (Bn,)), state.shape[0])
-    other = _other_stream(stream, dev, "ssd_delta_decode_step")
+    other = None if stream is None else _other_stream(stream, dev, "ssd_delta_decode_step")
     if y is None:
-        y = _made(other, lambda: (torch.empty if slots is None else torch.zeros)((Bn, H * P), dtype=dtype, device=dev))
+        y = _made(other, torch.empty if slots is None else torch.zeros, (Bn, H * P), dtype=dtype, device=dev)
     a = DeltaDecodeArgs(*rows, *_rows(y, "y", dtype, dev, (Bn, H * P)))
     _call(lib.ssd_delta_decode_step, "ssd_delta_decode_step", dev, other, ctypes.byref(c), ctypes.byref(a))
     return y
