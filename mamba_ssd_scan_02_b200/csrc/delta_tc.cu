@@ -92,7 +92,7 @@ constexpr uint32_t OFF_SB = OFF_VG + kDeep * kVG;
 constexpr uint32_t OFF_R = OFF_SB + 2 * kHalf;    // R operand of y: [token][32 p of each half], 64 rows
 constexpr uint32_t OFF_MAXS = OFF_R + 8192;       // largest |S| per chain warp: two chunks, an item's first
 constexpr uint32_t OFF_SCALE = OFF_MAXS + 128;    // per half and chunk parity: the scales of S and of y's R, backwards
-constexpr uint32_t OFF_BOUND = OFF_SCALE + 32;    // per place in the ring: 4 max |w V|, max |u V|, the first 2^cs, the last
+constexpr uint32_t OFF_BOUND = OFF_SCALE + 32;    // per place in the ring: max |w V|, max |u V|, the first 2^cs, the last
 constexpr uint32_t OFF_BAR = OFF_BOUND + 64;
 // A barrier that can complete again before every waiter has seen the phase before has one copy per
 // buffer, so that a parity test never sees two phases at once.
@@ -268,17 +268,19 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Powers of two that bring a quantity bounded by m to [64, 128) and back.  Headroom: with alpha <= 1
+// Powers of two that bring m to [2^(6 - kUp), 2^(7 - kUp)) and back.  Headroom: with alpha <= 1
 // and beta |k|^2 <= 2 the transition does not expand a state row s, so over a chunk
 // |s'| <= gamma |s| + 64 max |w V| max |K|, with |K| < 23 and, of 128 elements, |s| <= 12 max |S|; and
 // |w X| <= max |w V| + 2 gamma |s|, since w_j 2^{cs_j} rho_j |K_j| = gamma beta_j |k_j|^2 / |K_j| <= 2 gamma.  With
-// m = gamma max |S| + 4 max |w V| the next state and R are below 380 m.  The R of y is below 25 times the larger of
-// max |u V| and 2^{cs_0} max |S|, what the first token leaves of the state: all under 65504 / 128 = 511.
+// m = gamma max |S| / 4 + max |w V| and kUp = 2 the next state and R are below 1500 m.  The R of y is below 25 times
+// the larger of max |u V| and 2^{cs_0} max |S|, what the first token leaves of the state (kUp = 0).  Scaled, all are
+// under 65504.
 // Where m is infinite or NaN both are NaN, and so is then every state row: scaled by what is left of such a
 // bound, the rows without one in them would silently lose their bits.
+template <int kUp>
 __device__ __forceinline__ float2 state_scale(float m) {
   const int raw = (int)((__float_as_uint(m) >> 23) & 255u), e = min(max(raw, 8), 254);
-  const uint32_t to = (uint32_t)(260 - e) << 23, from = (uint32_t)(e - 6) << 23;
+  const uint32_t to = (uint32_t)(260 - kUp - e) << 23, from = (uint32_t)(e - 6 + kUp) << 23;
   return make_float2(__uint_as_float(raw == 255 ? 0x7fffffffu : to), __uint_as_float(raw == 255 ? 0x7fffffffu : from));
 }
 // (fmaxf would drop a NaN)
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float2 sc;
     uint32_t v[2][4];                  // the chunk's V, pairs
     float gr[2], u[2], w[2];           // of the chunk: 2^cs rho_k, u, w
-    float4 bound = make_float4(0.f, 0.f, 0.f, 0.f);  // 4 max |w V|, max |u V|, the first 2^cs, the last
+    float4 bound = make_float4(0.f, 0.f, 0.f, 0.f);  // max |w V|, max |u V|, the first 2^cs, the last
     Ring<kDeep> ring;  // of the rows to load next
     const auto load_rows = [&](int c) {
       const unsigned char *stage = smem + OFF_VG + ring.at * kVG;
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait(BAR_MAX + hf, maxes++ & 1);
         m = read_max(2);
       }
-      sc = state_scale(m);
+      sc = state_scale<0>(m);
 #pragma unroll
       for (int j = 0; j < 16; ++j) S[j] = __fmul2_rn(S[j], make_float2(sc.x, sc.x));
       ok = load_rows(0) && ok;
@@ -443,10 +445,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         publish_max(k & 1);
         ok = wait(BAR_MAX + hf, maxes++ & 1) && ok;
         // (A decay below 2^-126 is zero in 2^{cs_C}, but not yet in w_j 2^{cs_j}: it counts as that in the bound.  And S
-        // grows by at most 2^66 in its new scale, where zeros could otherwise meet an infinity.)
+        // grows by at most 2^64 in its new scale, where zeros could otherwise meet an infinity.)
         const float top = read_max(k & 1), decay = bound.w * sc.y, least = fmaxf(bound.w, 0x1p-126f) * sc.y;
-        const float2 nsc = state_scale(max_bound(fmaf(least, top, bound.x), 0x1p-60f * least));
-        const float2 ysc = state_scale(max_bound(bound.z * sc.y * top, bound.y));
+        const float2 nsc = state_scale<2>(max_bound(fmaf(0.25f * least, top, bound.x), 0x1p-60f * least));
+        const float2 ysc = state_scale<0>(max_bound(bound.z * sc.y * top, bound.y));
         ok = wait(BAR_D1, k & 1) && ok;
         __syncwarp();
         tc_fence_after();
@@ -591,13 +593,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int token = c * C + row + 8 * t;
-            const float g = gamma[t] * sc.x;
-            const float2 r2 = make_float2(rho[t], rho[t]), b2 = make_float2(sc.y, sc.y), g2 = make_float2(g, g);
+            // (rho first: without it the sums of the largest values would overflow)
+            const float g = gamma[t] * (sc.x * rho[t]), yb = sc.y * rho[t];
+            const float2 b2 = make_float2(yb, yb), g2 = make_float2(g, g);
             uint32_t u[4];
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
               const float2 w = __ffma2_rn(b2, make_float2(o[4 * b + 2 * t], o[4 * b + 2 * t + 1]), __fmul2_rn(g2, hold[hf][t][b]));
-              const __nv_bfloat162 x = __float22bfloat162_rn(__fmul2_rn(r2, w));
+              const __nv_bfloat162 x = __float22bfloat162_rn(w);
               u[b] = *reinterpret_cast<const uint32_t *>(&x);
             }
             // a row's four lanes exchange, so that lane l % 4 has the columns 8 (l % 4) ..: 16 bytes to store
@@ -770,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lead) {
           const float *gamma = reinterpret_cast<const float *>(stage + OFF_GAMMA);
           reinterpret_cast<float4 *>(smem + OFF_BOUND)[r.at] =
-              make_float4(4.f * __uint_as_float(top_w), __uint_as_float(top_u), gamma[0], gamma[C - 1]);
+              make_float4(__uint_as_float(top_w), __uint_as_float(top_u), gamma[0], gamma[C - 1]);
           mbar_arrive(BAR(BAR_READY + r.at));
         }
         __syncwarp();

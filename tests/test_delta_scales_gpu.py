@@ -203,3 +203,19 @@ def test_a_state_that_the_first_token_forgets(cuda_lib, kernel):
         d["dt"][t] = ref.store(np.full(4, 0.3), cfg)
     d["v"] = ref.store(1e-3 * ref.values(d["v"]), cfg)
     check_heads(cuda_lib, cfg, d, [0, 150], kernel)
+
+
+@pytest.mark.parametrize("kernel", [SIMT, TENSOR])
+@pytest.mark.parametrize("headdim", [64, 128])
+def test_the_largest_and_smallest_values(cuda_lib, headdim, kernel):
+    """Keys along an axis, values and states within a factor of four of what bf16 and fp32 hold, and near 2^-90."""
+    cfg = ref.config(headdim=headdim)
+    d = ref.inputs(cfg, 100, 1, seed=12)
+    k = np.zeros((100, 256))
+    k[np.arange(100), np.arange(100) % 128] = k[np.arange(100), 128 + np.arange(100) % 128] = 3.0
+    d["k"] = ref.store(k, cfg)
+    x = ref.values(d["v"])
+    for size in (8e37, 1e-27):
+        d["v"] = ref.store(np.clip(x, -1, 1) * size, cfg)
+        d["h0"] = (np.clip(d["h0"] / np.abs(d["h0"]).max(), -1, 1) * size).astype(np.float32)
+        check_heads(cuda_lib, cfg, d, [0, 100], kernel, f"{size}")
