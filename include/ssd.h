@@ -236,8 +236,10 @@ ssd_status_t mamba2_mixer_forward(const ssd_mixer_config_t *cfg, const ssd_mixer
  * [B, H, P, N] fp32, so the state cache below serves both.  alpha_t in [0, 1] (A <= 0) and
  * 0 <= beta_t |k^_t|^2 <= 2 keep the state bounded.  The chunked kernels need both (beyond them their 16-bit
  * operands can overflow, to NaN); the recurrence and the decode step compute other values as they
- * stand.  A NaN or an infinity in a token reaches every later y and state of its sequence and head (q: its
- * own y), and on the chunked kernels those of the token's chunk of 64 that come before it, too. */
+ * stand.  |q|^2 and |k|^2 are finite in fp32 (elements below about 1e18).  A NaN or an infinity in a token
+ * reaches every later y and state of its sequence and head (q: its own y), and on the chunked kernels those of the
+ * token's chunk of 64 that come before it, too.  In h0 it reaches its own row of the state; on the chunked kernels
+ * an infinity reaches the 32 rows around it. */
 typedef struct {
   int batch;        /* B >= 1 */
   int seqlen;       /* L >= 0 tokens in this call (0: h0, or zeros, goes to h_final); ignored by
@@ -307,8 +309,8 @@ ssd_status_t ssd_delta_prefill(const ssd_delta_config_t *cfg, const ssd_delta_ar
 
 /* Packed sequences, as in ssd_prefill_varlen: cu_seqlens is a HOST array of nseq + 1 offsets (read
  * before the call returns, a stream capture included), cfg->batch = 1, cfg->seqlen = all tokens,
- * h0 / h_final [nseq, H, P, N].  One launch of each kernel for the whole batch.  An empty sequence's
- * h0 (or zeros) goes to its h_final.  ssd_delta_varlen_workspace_size is 0 for invalid arguments. */
+ * h0 / h_final [nseq, H, P, N].  One launch of each kernel for the whole batch, and one per 320 sequences that
+ * brings the offsets to the device.  An empty sequence's h0 (or zeros) goes to its h_final bit by bit.  ssd_delta_varlen_workspace_size is 0 for invalid arguments. */
 size_t ssd_delta_varlen_workspace_size(const ssd_delta_config_t *cfg, const int *cu_seqlens, int nseq);
 ssd_status_t ssd_delta_prefill_varlen(const ssd_delta_config_t *cfg, const ssd_delta_args_t *args,
                                       const int *cu_seqlens, int nseq, void *stream);

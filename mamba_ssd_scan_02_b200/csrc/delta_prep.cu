@@ -14,7 +14,7 @@
 //
 // Why apart from the chunk kernel: inside it this part ran in the same SM as the tcgen05 products, which
 // slow mma.sync down threefold and shared-memory loads twofold, and its latency (about 5 us a chunk)
-// bounded every CTA: 650 us for 8192 tokens x 128 heads, where the two kernels now take 121 and 220.  Here it
+// bounded every CTA: 650 us for 8192 tokens x 128 heads, where the two kernels now take 121 and 228.  Here it
 // is spread over all chunks, twelve independent warps per SM (three CTAs; two of them with rows of one
 // pitch: 154 us).  The price is 16 KB of workspace per chunk and head, written once and read once.
 //

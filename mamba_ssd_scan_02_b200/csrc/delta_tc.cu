@@ -15,13 +15,15 @@
 // to chunk is two dependent products, K S^T (which gives R = w X) and M R.  A CTA carries 64 state rows of one head
 // through a sequence (the rows are independent given K, so a head of 128 rows is two such items), then the next
 // item's: the grid is one CTA per SM, and an item's first loads and M run while the one before ends (64
-// sequences of up to 700 tokens x 128 heads: 715 us with a CTA per item, 610 so).
+// sequences of up to 700 tokens x 128 heads, when the chunks were slower than now: 715 us with a CTA per item, 606 so;
+// now 572).
 //
 // The front end (delta_prep.cu) computes T~, A T = 2^{cs_t - cs_j} (A~ T~)_tj, u and w.
 //
 // Precision.  The state is fp32, in registers.  Its products run on fp16 operands in two parts,
 // hi = fp16(x), lo = fp16(x - hi), which keep 22 bits; the products hi.hi + hi.lo + lo.hi leave an error
-// of about 2^-22, so the state stays as near to the fp64 rule as an fp32 recurrence does.  K and Q need
+// of about 2^-22, so the state stays as near to the fp64 rule as an fp32 recurrence does (2.3e-7 of its root mean
+// square after 8192 tokens, the worst of 128 heads 3.1e-7).  K and Q need
 // one part: a row of bf16 numbers times a power of two is exact in fp16, and the power and the norm's
 // factor come back in the fp32 factors rho.  What differs in size between tokens and heads - beta, the decays, the
 // rho - stands in R, in fp32 before it is split: |T~|, |M| and |A T| are bounded without it (beta |k|^2 <= 2, 1 <=
@@ -29,21 +31,22 @@
 // counts each token's value as what is left of it at the chunk's end (state_scale).  So a term loses bits only
 // beside larger terms of the same state.  (With the factors in M, which had no scale, and R's scale from |S| and |V|
 // alone, a chunk that ended in tokens of small beta or without values lost up to all of the state's bits.)  Only
-// what goes into y alone (A~, A T, the R beside it: u X, scaled by the largest |S| and |u V|) is rounded to 11 bits,
-// each product below 2^-24 of the chunk's largest to fewer: y is then rounded to bf16's 8.
+// what goes into y alone (A~, A T, the R beside it: u X, scaled by the largest |u V| and what the first token leaves
+// of the largest |S|) is rounded to 11 bits, and to 2^-24 of the chunk's largest term where that is more: y is then
+// rounded to bf16's 8.
 //
 // Roles (16 warps, so that a thread may have 128 registers).  Warps 0-7, the chain: S into its operand, R
 // from K S^T, the new S.  Their two halves, 32 state rows each, share the product with K, whose operand is
 // read once for both, and have M R each, so that one converts while the other's runs.  Warps 8-11 bring M (of
 // the chunk after) into its operand and make y from Q S^T and A T R, neither in the chain's way.  Warp 12
-// issues the MMAs of the chains, warp 13 those of M, warp 14 loads, warp 15 loads T and finds the largest |V|
-// of each chunk.  Hand-overs are mbarriers; every wait is bounded: a timeout makes every role leave and
+// issues the MMAs of the chains, warp 13 those of M, warp 14 loads, warp 15 loads T and finds the largest |w V| and
+// |u V| of each chunk.  Hand-overs are mbarriers; every wait is bounded: a timeout makes every role leave and
 // latches SSD_ERR_TIMEOUT.
 //
-// What bounds it: the chain.  A chunk takes 1.7 us (8192 tokens x 128 heads: 220 us on 128 SMs; 245 at the clocks
-// that a second of such calls leaves): S into fp16 0.25 (the halves one after the other 0.5), K S^T 0.4, R 0.25,
-// M R 0.35 (the next rows load meanwhile), the new S 0.2; the tensor pipe is 53 % busy, the issue slots 59 %, DRAM
-// 27 %.  Measured against it, at the stage each was tried: y by the chain's warps 246 us where this took 226;
+// What bounds it: the chain.  A chunk takes 1.8 us (8192 tokens x 128 heads: 228 us on 128 SMs, and 220 with one R for
+// the state and y, whose scales then left bits out).  Of those 220: S into fp16 0.25 (the halves one after the other
+// 0.5), K S^T 0.4, R 0.25, M R 0.35 (the next rows load meanwhile), the new S 0.2.  Now the tensor pipe is 50 % busy,
+// the issue slots 59 %, DRAM 27 %.  Measured against it, at the stage each was tried: y by the chain's warps 246 us where this took 226;
 // M R waiting for the readers of Q S^T 226 : 213; one M R for both halves 246 : 226; a product per half for
 // K S^T (the halves half a chunk apart, one issuer each or one for both) 255 to 260 : 232, since the K and Q
 // operand is then read twice.  The code is kept small (loops rolled, one place per inlined part): sixteen
