@@ -6,7 +6,7 @@ from tests.test_delta_gpu import SIMT, TENSOR, on_gpu, run_packed
 
 pytestmark = pytest.mark.gpu
 
-CYCLES = 200_000_000  # of a busy stream: a tenth of a second
+CYCLES = 800_000_000  # of a busy stream: four tenths of a second
 
 
 def held_back(shapes, cycles=CYCLES):
