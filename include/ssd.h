@@ -310,7 +310,8 @@ ssd_status_t ssd_delta_prefill(const ssd_delta_config_t *cfg, const ssd_delta_ar
 /* Packed sequences, as in ssd_prefill_varlen: cu_seqlens is a HOST array of nseq + 1 offsets (read
  * before the call returns, a stream capture included), cfg->batch = 1, cfg->seqlen = all tokens,
  * h0 / h_final [nseq, H, P, N].  One launch of each kernel for the whole batch, and one per 320 sequences that
- * brings the offsets to the device.  An empty sequence's h0 (or zeros) goes to its h_final bit by bit.  ssd_delta_varlen_workspace_size is 0 for invalid arguments. */
+ * brings the offsets to the device.  An empty sequence's h0 (or zeros) goes to its h_final bit by bit.
+ * ssd_delta_varlen_workspace_size is 0 for invalid arguments. */
 size_t ssd_delta_varlen_workspace_size(const ssd_delta_config_t *cfg, const int *cu_seqlens, int nseq);
 ssd_status_t ssd_delta_prefill_varlen(const ssd_delta_config_t *cfg, const ssd_delta_args_t *args,
                                       const int *cu_seqlens, int nseq, void *stream);
